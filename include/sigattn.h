@@ -372,6 +372,66 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
                                     sigattn_stream stream);
 
 /*
+ * Norm of each query and key head with the position rotation in the same pass: what a layer
+ * does to the outputs of its projections before sigattn_fwd.  Per
+ * valid token and head, x the head's d values:
+ *     u = x / sqrt(mean(x^2) + eps)   (norm = 1; norm = 0: u = x and eps is not used)
+ *     y = R (w * u)                   w fp32 [d], shared by the tensor's heads; NULL: all 1
+ * R turns the pairs of the first rot_dim values (a multiple of 16 up to d; 0: no rotation)
+ * and passes the others: pair p (a, b) becomes (a cos t - b sin t, a sin t + b cos t) with
+ * t = position * inv_freq[p].  interleaved 0: pair p is (x[p], x[p + rot_dim/2]); 1: it is
+ * (x[2p], x[2p + 1]).  Positions have 1 to 4 axes (time, height, width ...): sections (a
+ * HOST array of `axes` counts that add up to rot_dim/2) says how many consecutive pairs each
+ * axis turns.  positions: device int32, of axis a, batch entry b and row i at
+ * a * pos_stride_axis + b * pos_stride_b + i, any value, negative ones included; angles are
+ * taken modulo a turn in 64 bits, so they are as exact far out as near.  inv_freq: device
+ * fp64 [rot_dim/2], radians per position.
+ *
+ * Tensors are bf16 [B, N, H, d] with strides, pointers and alignment as above (d = 64 or
+ * 128); q has Hq heads and k Hk, any numbers; either may be 0 and its pointers NULL.  A
+ * packed [T, H, d] batch is B = 1, N = T.  lengths: device int32 [B] or NULL (all N rows are
+ * valid); rows at or past a sequence's length are not read and come out as exactly 0.  An
+ * output may be the very tensor it is computed from (same pointer and strides); otherwise
+ * inputs and outputs must not overlap, nor an output's elements one another.
+ *
+ * Backward: from dyq, dyk writes dq, dk (bf16; pad rows 0) and, where the pointers are not
+ * NULL, dwq and dwk (fp32 [d], sums over all valid rows and heads, in an order that does not
+ * change from run to run).  x is read again and nothing else of the forward is needed.
+ * workspace: needed for dwq / dwk only, sigattn_qk_norm_rope_bwd_workspace_size() bytes,
+ * 16-byte aligned, contents free on entry and undefined after; calls sharing one must not
+ * overlap on the GPU.
+ * Errors: INVALID (null pointer, B or N < 1, no heads, norm / interleaved not 0 or 1,
+ * negative eps or stride, sections that do not add up, workspace missing or too small),
+ * UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past 2^31 - 2^14), ALIGNMENT, CUDA.
+ */
+SIGATTN_API int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const int32_t* lengths,
+                                     const void* q, const int64_t q_strides[3],
+                                     const void* k, const int64_t k_strides[3],
+                                     const float* wq, const float* wk, int norm, float eps,
+                                     int rot_dim, int interleaved, int axes,
+                                     const int32_t* sections, const double* inv_freq,
+                                     const int32_t* positions, int64_t pos_stride_axis,
+                                     int64_t pos_stride_b, void* yq, const int64_t yq_strides[3],
+                                     void* yk, const int64_t yk_strides[3],
+                                     sigattn_stream stream);
+SIGATTN_API int sigattn_qk_norm_rope_bwd_workspace_size(int B, int N, int d, size_t* bytes);
+SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
+                                         const int32_t* lengths,
+                                         const void* q, const int64_t q_strides[3],
+                                         const void* k, const int64_t k_strides[3],
+                                         const void* dyq, const int64_t dyq_strides[3],
+                                         const void* dyk, const int64_t dyk_strides[3],
+                                         const float* wq, const float* wk, int norm, float eps,
+                                         int rot_dim, int interleaved, int axes,
+                                         const int32_t* sections, const double* inv_freq,
+                                         const int32_t* positions, int64_t pos_stride_axis,
+                                         int64_t pos_stride_b,
+                                         void* dq, const int64_t dq_strides[3],
+                                         void* dk, const int64_t dk_strides[3],
+                                         float* dwq, float* dwk, void* workspace,
+                                         size_t workspace_bytes, sigattn_stream stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device status word of the current
  * device: SIGATTN_OK, or SIGATTN_ERR_TIMEOUT if a kernel's bounded wait expired since the
  * last call (that kernel's outputs are then undefined), or SIGATTN_ERR_CUDA.

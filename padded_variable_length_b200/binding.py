@@ -87,6 +87,12 @@ _sig("sigattn_bwd_fused_workspace_size", ctypes.c_int, _p, ctypes.c_int, ctypes.
 _sig("sigattn_bwd_fused", ctypes.c_int, _p, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
      _p, _I64x3, _p, _I64x3, _p, _I64x3, _p, _I64x3, _p, _I64x3, _p, _i64, _p, _p, ctypes.c_size_t,
      _p, _I64x3, _p, _I64x3, _p, _I64x3, _p)
+_qk_rot = [_p, _p, ctypes.c_int, ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_i32), _p,
+           _p, _i64, _i64]
+_sig("sigattn_qk_norm_rope", ctypes.c_int, *[ctypes.c_int] * 5, _p, *[_p, _I64x3] * 2, *_qk_rot, *[_p, _I64x3] * 2, _p)
+_sig("sigattn_qk_norm_rope_bwd_workspace_size", ctypes.c_int, *[ctypes.c_int] * 3, ctypes.POINTER(ctypes.c_size_t))
+_sig("sigattn_qk_norm_rope_bwd", ctypes.c_int, *[ctypes.c_int] * 5, _p, *[_p, _I64x3] * 4, *_qk_rot, *[_p, _I64x3] * 2,
+     _p, _p, _p, ctypes.c_size_t, _p)
 _sig("sigattn_get_status", ctypes.c_int, _p)
 _sig("sigattn_set_wait_limit_ns", ctypes.c_int, _u64)
 _sig("sigattn_selftest_wait_timeout", ctypes.c_int, _u64, _p)
@@ -417,6 +423,169 @@ def bwd_fused(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, ls
                                   dq.data_ptr(), _strides(dq), dk.data_ptr(), _strides(dk),
                                   dv.data_ptr(), _strides(dv), _stream(stream)), "bwd_fused")
     return dq, dk, dv
+
+
+# --------------------------------------------------------------------------------------
+# Norm and rotation of queries and keys
+# --------------------------------------------------------------------------------------
+def _tensor(t, name: str, dim=(3, 4)) -> torch.Tensor:
+    """A bf16 CUDA tensor on the current device, d contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() not in dim:
+        raise ValueError(f"{name} must be a bf16 tensor of {' or '.join(map(str, dim))} dimensions")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _on_device(t, name)
+
+
+def _on_device(t: torch.Tensor, name: str) -> torch.Tensor:
+    """Kernels run on the current device: a tensor that lives elsewhere is refused."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t
+
+
+def _small(t, name: str, dtype, shape) -> Optional[int]:
+    """Pointer of a contiguous tensor of exactly this type and shape (None passes)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return _on_device(t, name).data_ptr()
+
+
+def _extent_strides(t: torch.Tensor) -> ctypes.Array:
+    """(batch, token, head) strides; the stride of a dimension of one entry is never used, so
+    whatever it is, 0 is passed."""
+    s = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)][:-1]
+    return _I64x3(*([0] * (3 - len(s)) + s))
+
+
+def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
+    """The output tensor: a new one, or the caller's after the checks that an output needs."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _tensor(t, name, (like.dim(),))
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    if any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return t
+
+
+def _workspace(workspace, need: int, like: torch.Tensor):
+    """(tensor, pointer, bytes): the caller's buffer, or a new one of `need` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty((need + 3) // 4, dtype=torch.float32, device=like.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on_device(workspace, "workspace")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm):
+    """The arguments that both directions of qk_norm_rope share, checked: (shape arguments,
+    norm and rotation arguments, whatever must stay alive until the call)."""
+    if q is None and k is None:
+        raise ValueError("q or k is needed")
+    for t, name in ((q, "q"), (k, "k")):
+        if t is not None:
+            _tensor(t, name)
+    t = q if q is not None else k
+    if q is not None and k is not None and (q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]):
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must agree in all but the heads")
+    rows = tuple(t.shape[:-2])
+    B, N, d = (1 if t.dim() == 3 else t.shape[0]), t.shape[-3], t.shape[-1]
+    lp = _small(lengths, "lengths", torch.int32, (B,))
+    if lengths is not None and t.dim() == 3:
+        raise ValueError("a packed batch has no lengths: all of its rows are valid")
+    wp = [_small(w, name, torch.float32, (d,)) for w, name in ((wq, "wq"), (wk, "wk"))]
+    rot, sec, ip, pp, sa, sb = 0, None, None, None, 0, 0
+    if inv_freq is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        if inv_freq.dim() != 1 or inv_freq.shape[0] < 1:
+            raise ValueError("inv_freq must be a tensor [rot_dim / 2]")
+        ip = _small(inv_freq, "inv_freq", torch.float64, inv_freq.shape)
+        rot = 2 * inv_freq.shape[0]
+        sec = [int(x) for x in sections] if sections is not None else [rot // 2]
+        if len(sec) < 1 or sum(sec) != rot // 2 or min(sec) < 0:
+            raise ValueError(f"sections must be counts that add up to {rot // 2}")
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+            raise ValueError("positions must be an int32 tensor")
+        if len(sec) == 1 and tuple(positions.shape) == rows:
+            positions = positions[None]
+        if tuple(positions.shape) != (len(sec),) + rows:
+            raise ValueError(f"positions must have shape {(len(sec),) + rows}")
+        if positions.stride(-1) != 1 and positions.shape[-1] > 1:
+            raise ValueError("positions: the rows must be contiguous")
+        pp = _on_device(positions, "positions").data_ptr()
+        sa, sb = positions.stride(0), (positions.stride(1) if positions.dim() == 3 else 0)
+    elif positions is not None or sections is not None:
+        raise ValueError("positions and sections need inv_freq")
+    n_sec = len(sec) if sec else 0
+    c_sec = (_i32 * n_sec)(*sec) if sec else None
+    heads = [0 if x is None else x.shape[-2] for x in (q, k)]
+    return ((B, N, heads[0], heads[1], d, lp),
+            (wp[0], wp[1], int(bool(norm)), float(eps), rot, int(bool(interleaved)), n_sec, c_sec, ip, pp, sa, sb),
+            (positions, c_sec))
+
+
+def _pair(t):
+    return (None, _I64x3(0, 0, 0)) if t is None else (t.data_ptr(), _extent_strides(t))
+
+
+def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None, sections=None,
+                 interleaved: bool = False, lengths=None, norm: bool = True, out_q=None, out_k=None, stream=None):
+    """(yq, yk): every head of q and k normed by its root mean square (norm=False: not),
+    weighted, and its first 2 * len(inv_freq) values rotated by the positions.  q, k bf16
+    [B, N, H, d] or packed [T, H, d] (either may be None); wq, wk fp32 [d]; inv_freq fp64
+    [pairs]; positions int32 [axes, B, N] resp. [axes, T] (one axis: that dimension may be
+    left out); sections: pairs of each axis.  Pad rows (lengths int32 [B]) come out as 0."""
+    head, rot, alive = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm)
+    yq = None if q is None else _out(out_q, q, "out_q")
+    yk = None if k is None else _out(out_k, k, "out_k")
+    if head[0] * head[1] * (head[2] + head[3]) > 0:
+        _check(_lib.sigattn_qk_norm_rope(*head, *_pair(q), *_pair(k), *rot, *_pair(yq), *_pair(yk), _stream(stream)),
+               "qk_norm_rope")
+    return yq, yk
+
+
+def qk_norm_rope_bwd_workspace_bytes(B: int, N: int, d: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.sigattn_qk_norm_rope_bwd_workspace_size(B, N, d, ctypes.byref(n)), "qk_norm_rope_bwd_workspace_size")
+    return n.value
+
+
+def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None,
+                     sections=None, interleaved: bool = False, lengths=None, norm: bool = True, dq=None, dk=None,
+                     workspace=None, stream=None):
+    """(dq, dk, dwq, dwk) from the gradients dyq, dyk of qk_norm_rope's outputs; dwq, dwk are
+    fp32 [d], None for a weight that is None.  ``workspace``: a contiguous CUDA buffer of
+    qk_norm_rope_bwd_workspace_bytes bytes (allocated here if None and needed)."""
+    head, rot, alive = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm)
+    outs, grads = [], []
+    for x, dy, w, dx, name in ((q, dyq, wq, dq, "q"), (k, dyk, wk, dk, "k")):
+        if x is None:
+            if dy is not None or w is not None or dx is not None:
+                raise ValueError(f"gradients or weights of an absent {name}")
+            outs.append(None)
+            grads.append(None)
+            continue
+        if _tensor(dy, "dy" + name, (x.dim(),)).shape != x.shape:
+            raise ValueError(f"dy{name} must have shape {tuple(x.shape)}")
+        outs.append(_out(dx, x, "d" + name))
+        grads.append(None if w is None else torch.empty_like(w))
+    if head[0] * head[1] * (head[2] + head[3]) == 0:
+        return outs[0], outs[1], *(None if g is None else g.zero_() for g in grads)
+    need = qk_norm_rope_bwd_workspace_bytes(head[0], head[1], head[4]) if any(g is not None for g in grads) else 0
+    ws, wp, wn = _workspace(workspace, need, outs[0] if outs[0] is not None else outs[1])
+    ptr = lambda g: None if g is None else g.data_ptr()
+    _check(_lib.sigattn_qk_norm_rope_bwd(*head, *_pair(q), *_pair(k), *_pair(dyq), *_pair(dyk), *rot,
+                                         *_pair(outs[0]), *_pair(outs[1]), ptr(grads[0]), ptr(grads[1]), wp, wn,
+                                         _stream(stream)), "qk_norm_rope_bwd")
+    return outs[0], outs[1], grads[0], grads[1]
 
 
 def get_status(stream=None) -> int:

@@ -1,6 +1,6 @@
 // C ABI of libsigattn.so: argument checks, TMA descriptors, the device status word, and
 // the small helper kernels (bias, bounded-wait self-test).  The attention kernels live in
-// fwd.cu and bwd.cu, the planner in plan.cu.
+// fwd.cu and bwd.cu, the planner in plan.cu and the query / key norm in qknorm.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
