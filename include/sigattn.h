@@ -373,7 +373,7 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
 
 /*
  * Norm of each query and key head with the position rotation in the same pass: what a layer
- * does to the outputs of its projections before sigattn_fwd.  Per
+ * does to the outputs of its projections before sigattn_fwd or sigattn_linear_fwd.  Per
  * valid token and head, x the head's d values:
  *     u = x / sqrt(mean(x^2) + eps)   (norm = 1; norm = 0: u = x and eps is not used)
  *     y = R (w * u)                   w fp32 [d], shared by the tensor's heads; NULL: all 1
@@ -430,6 +430,74 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
                                          void* dk, const int64_t dk_strides[3],
                                          float* dwq, float* dwk, void* workspace,
                                          size_t workspace_bytes, sigattn_stream stream);
+
+/*
+ * Linear attention with a decay per head: causal within each sequence, no normaliser, and a
+ * d x d state per (sequence, head) instead of the keys and values:
+ *     S_t = lambda S_{t-1} + k_t v_t^T      lambda = exp(log_decay[h])
+ *     o_t = scale S_t^T q_t
+ * log_decay: device fp32 [H], at most 0 (above 0, or NaN, counts as 0; -inf is lambda = 0).
+ * state: fp32 [B, H, d, d] (rows along k, columns along v), S before each sequence's first
+ * token, or NULL for 0; final_state: the same layout, S after its last one (the state itself
+ * for an empty sequence), or NULL.  They may be the same buffer.
+ *
+ * Batches, like the attention calls' but without a plan: with cu_seqlens NULL, padded
+ * [B, N, H, d] tensors, sequence b has lengths[b] rows (device int32 [B], clamped into
+ * [0, N]; NULL: all N) and its pad rows come out as exactly 0, whatever they hold (NaN
+ * included).  With cu_seqlens (device int32 [B + 1], non-decreasing; lengths must be NULL),
+ * packed [T, H, d] tensors, sequence b in rows cu_seqlens[b] .. cu_seqlens[b + 1]; N is the
+ * longest sequence (a longer one is cut there) and rows of no sequence are not written.
+ * Pointers, strides and d (64, 128) as above; states and workspace 16-byte aligned.
+ * Inputs are bf16 and accumulated in fp32; the state is kept in fp32.
+ *
+ * workspace: sigattn_linear_workspace_size() bytes (0 where B and H alone fill the GPU:
+ * then it may be NULL), contents free on entry and undefined after; calls sharing one must
+ * not overlap on the GPU.  Results do not change from run to run.
+ *
+ * Backward of L = sum(do * o) + sum(dfinal_state * final_state): writes dq, dk, dv (bf16, pad
+ * rows 0) and, where dstate is not NULL, dL/dstate (fp32).  dfinal_state NULL means 0;
+ * dstate may be the same buffer as dfinal_state.  log_decay has no gradient.
+ *
+ * Errors: INVALID (null pointer, B, N, H or T < 1, both lengths and cu_seqlens, non-finite
+ * scale, workspace missing or too small), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT,
+ * NO_DEVICE, CUDA; TIMEOUT through sigattn_get_status.
+ */
+SIGATTN_API int sigattn_linear_workspace_size(int B, int N, int H, int d, int backward,
+                                              size_t* bytes);
+SIGATTN_API int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                   const int32_t* cu_seqlens, const float* log_decay, float scale,
+                                   const void* q, const int64_t q_strides[3],
+                                   const void* k, const int64_t k_strides[3],
+                                   const void* v, const int64_t v_strides[3],
+                                   const float* state, void* o, const int64_t o_strides[3],
+                                   float* final_state, void* workspace, size_t workspace_bytes,
+                                   sigattn_stream stream);
+SIGATTN_API int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                   const int32_t* cu_seqlens, const float* log_decay, float scale,
+                                   const void* q, const int64_t q_strides[3],
+                                   const void* k, const int64_t k_strides[3],
+                                   const void* v, const int64_t v_strides[3],
+                                   const void* dout, const int64_t do_strides[3],
+                                   const float* state, const float* dfinal_state,
+                                   void* dq, const int64_t dq_strides[3],
+                                   void* dk, const int64_t dk_strides[3],
+                                   void* dv, const int64_t dv_strides[3],
+                                   float* dstate, void* workspace, size_t workspace_bytes,
+                                   sigattn_stream stream);
+
+/*
+ * One token of each sequence: q, k, v, o bf16 with d contiguous and {batch, head} strides
+ * (any non-negative ones), state and state_out fp32 [B, H, d, d], the same buffer (the state
+ * is updated in place) or not overlapping.  Sequence b with lengths[b] < 1 (lengths NULL:
+ * none) has no token: o is 0 and its state stays.  Errors as sigattn_linear_fwd.
+ */
+SIGATTN_API int sigattn_linear_step(int B, int H, int d, const int32_t* lengths,
+                                    const float* log_decay, float scale,
+                                    const void* q, const int64_t q_strides[2],
+                                    const void* k, const int64_t k_strides[2],
+                                    const void* v, const int64_t v_strides[2],
+                                    const float* state, float* state_out,
+                                    void* o, const int64_t o_strides[2], sigattn_stream stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of the current

@@ -93,6 +93,14 @@ _sig("sigattn_qk_norm_rope", ctypes.c_int, *[ctypes.c_int] * 5, _p, *[_p, _I64x3
 _sig("sigattn_qk_norm_rope_bwd_workspace_size", ctypes.c_int, *[ctypes.c_int] * 3, ctypes.POINTER(ctypes.c_size_t))
 _sig("sigattn_qk_norm_rope_bwd", ctypes.c_int, *[ctypes.c_int] * 5, _p, *[_p, _I64x3] * 4, *_qk_rot, *[_p, _I64x3] * 2,
      _p, _p, _p, ctypes.c_size_t, _p)
+_I64x2 = ctypes.c_int64 * 2
+_sig("sigattn_linear_workspace_size", ctypes.c_int, *[ctypes.c_int] * 5, ctypes.POINTER(ctypes.c_size_t))
+_sig("sigattn_linear_fwd", ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, _p, _p, _p,
+     ctypes.c_float, *[_p, _I64x3] * 3, _p, _p, _I64x3, _p, _p, ctypes.c_size_t, _p)
+_sig("sigattn_linear_bwd", ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, _p, _p, _p,
+     ctypes.c_float, *[_p, _I64x3] * 4, _p, _p, *[_p, _I64x3] * 3, _p, _p, ctypes.c_size_t, _p)
+_sig("sigattn_linear_step", ctypes.c_int, *[ctypes.c_int] * 3, _p, _p, ctypes.c_float, *[_p, _I64x2] * 3, _p, _p,
+     _p, _I64x2, _p)
 _sig("sigattn_get_status", ctypes.c_int, _p)
 _sig("sigattn_set_wait_limit_ns", ctypes.c_int, _u64)
 _sig("sigattn_selftest_wait_timeout", ctypes.c_int, _u64, _p)
@@ -426,7 +434,7 @@ def bwd_fused(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, ls
 
 
 # --------------------------------------------------------------------------------------
-# Norm and rotation of queries and keys
+# Norm and rotation of queries and keys; linear attention
 # --------------------------------------------------------------------------------------
 def _tensor(t, name: str, dim=(3, 4)) -> torch.Tensor:
     """A bf16 CUDA tensor on the current device, d contiguous."""
@@ -586,6 +594,108 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
                                          *_pair(outs[0]), *_pair(outs[1]), ptr(grads[0]), ptr(grads[1]), wp, wn,
                                          _stream(stream)), "qk_norm_rope_bwd")
     return outs[0], outs[1], grads[0], grads[1]
+
+
+def linear_workspace_bytes(B: int, N: int, H: int, d: int, backward: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.sigattn_linear_workspace_size(B, N, H, d, int(bool(backward)), ctypes.byref(n)), "linear_workspace_size")
+    return n.value
+
+
+def _linear_args(tensors, log_decay, lengths, cu_seqlens, max_seqlen, states):
+    """The shape arguments that linear_fwd and linear_bwd share, checked."""
+    q = tensors[0][0]
+    for t, name in tensors:
+        _tensor(t, name, (q.dim(),) if isinstance(q, torch.Tensor) and q.dim() in (3, 4) else (3, 4))
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must have q's shape {tuple(q.shape)}")
+    H, d = q.shape[-2:]
+    lp = cp = None
+    if q.dim() == 3:
+        if cu_seqlens is None or max_seqlen is None or lengths is not None:
+            raise ValueError("a packed batch takes cu_seqlens and max_seqlen, no lengths")
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor [B + 1]")
+        cp = _small(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape)
+        B, N, T = cu_seqlens.shape[0] - 1, int(max_seqlen), q.shape[0]
+    else:
+        if cu_seqlens is not None or max_seqlen is not None:
+            raise ValueError("a padded batch takes lengths, no cu_seqlens or max_seqlen")
+        B, N, T = q.shape[0], q.shape[1], 0
+        lp = _small(lengths, "lengths", torch.int32, (B,))
+    gp = _small(log_decay, "log_decay", torch.float32, (H,))
+    if gp is None:
+        raise ValueError("log_decay is needed")
+    ptrs = [_small(s, name, torch.float32, (B, H, d, d)) for s, name in states]
+    return (B, N, T, H, d, lp, cp, gp), ptrs
+
+
+def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None,
+               return_state: bool = False, scale: Optional[float] = None, out=None, final_state=None,
+               workspace=None, stream=None):
+    """(o, final_state) of linear attention with the decay exp(log_decay[h]): S = decay S +
+    k v^T, o = scale S^T q for each token in turn.  q, k, v bf16 [B, N, H, d] (with lengths) or
+    packed [T, H, d] (with cu_seqlens and max_seqlen); state fp32 [B, H, d, d] is what the
+    sequences start from (None: 0).  The final state is returned where return_state is set or
+    a buffer for it is given, else None."""
+    head, (sp, fp) = _linear_args(((q, "q"), (k, "k"), (v, "v")), log_decay, lengths, cu_seqlens, max_seqlen,
+                                  ((state, "state"), (final_state, "final_state")))
+    B, N, _, H, d = head[:5]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out = _out(out, q, "out")
+    if return_state and final_state is None:
+        final_state = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+        fp = final_state.data_ptr()
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q)
+    _check(_lib.sigattn_linear_fwd(*head, float(scale), *_pair(q), *_pair(k), *_pair(v), sp, *_pair(out), fp, wp, wn,
+                                   _stream(stream)), "linear_fwd")
+    return out, final_state
+
+
+def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None, dstate=None,
+               scale: Optional[float] = None, dq=None, dk=None, dv=None, dstate_out=None, workspace=None, stream=None):
+    """(dq, dk, dv, dstate_out): gradients of linear_fwd from do and, for a loss that uses the
+    final state, its gradient ``dstate``.  dstate_out, the gradient of ``state``, is None where
+    there was no state (unless a buffer for it is given)."""
+    head, (sp, ep, gp) = _linear_args(((q, "q"), (k, "k"), (v, "v"), (do, "do")), log_decay, lengths, cu_seqlens,
+                                      max_seqlen, ((state, "state"), (dstate, "dstate"), (dstate_out, "dstate_out")))
+    B, N, _, H, d = head[:5]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    dq, dk, dv = _out(dq, q, "dq"), _out(dk, k, "dk"), _out(dv, v, "dv")
+    if state is not None and dstate_out is None:
+        dstate_out = torch.empty_like(state)
+        gp = dstate_out.data_ptr()
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q)
+    _check(_lib.sigattn_linear_bwd(*head, float(scale), *_pair(q), *_pair(k), *_pair(v), *_pair(do), sp, ep,
+                                   *_pair(dq), *_pair(dk), *_pair(dv), gp, wp, wn, _stream(stream)), "linear_bwd")
+    return dq, dk, dv, dstate_out
+
+
+def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] = None, state_out=None, out=None,
+                stream=None) -> torch.Tensor:
+    """o of one token of each sequence, q, k, v bf16 [B, H, d]; ``state`` fp32 [B, H, d, d] is
+    updated in place, or kept and its update written to ``state_out``.  Sequences with
+    lengths[b] = 0 have no token: o is 0 and their state stays."""
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _tensor(t, name, (3,))
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must have q's shape {tuple(q.shape)}")
+    B, H, d = q.shape
+    lp = _small(lengths, "lengths", torch.int32, (B,))
+    gp = _small(log_decay, "log_decay", torch.float32, (H,))
+    sp = _small(state, "state", torch.float32, (B, H, d, d))
+    if gp is None or sp is None:
+        raise ValueError("log_decay and state are needed")
+    np_ = sp if state_out is None else _small(state_out, "state_out", torch.float32, (B, H, d, d))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out = _out(out, q, "out")
+    two = lambda t: (t.data_ptr(), _I64x2(*[st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)][:2]))
+    _check(_lib.sigattn_linear_step(B, H, d, lp, gp, float(scale), *two(q), *two(k), *two(v), sp, np_, *two(out),
+                                    _stream(stream)), "linear_step")
+    return out
 
 
 def get_status(stream=None) -> int:

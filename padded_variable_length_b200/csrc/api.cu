@@ -1,6 +1,7 @@
 // C ABI of libsigattn.so: argument checks, TMA descriptors, the device status word, and
 // the small helper kernels (bias, bounded-wait self-test).  The attention kernels live in
-// fwd.cu and bwd.cu, the planner in plan.cu and the query / key norm in qknorm.cu.
+// fwd.cu and bwd.cu, the planner in plan.cu, the query / key norm in qknorm.cu and linear
+// attention in linear.cu.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -136,6 +137,8 @@ __global__ void k_wait_selftest(int* status, unsigned long long limit_ns) {
 }
 
 }  // namespace
+
+unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 int make_tmap_bf16(CUtensorMap* map, const TensorDesc& t, int B, int H, int d) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();

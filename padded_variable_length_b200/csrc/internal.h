@@ -120,6 +120,9 @@ int make_tmap_f32_acc(CUtensorMap* map, float* base, int B, int N, int H, int d)
 
 int cuda_status(cudaError_t e);
 
+// The limit of the kernels' bounded waits (sigattn_set_wait_limit_ns).
+unsigned long long wait_limit_ns();
+
 // Device address of this device's status word (the record of bounded waits that gave up).
 int status_ptr(int** out);
 

@@ -1,0 +1,994 @@
+// Linear attention with a decay per head, over padded or packed variable-length batches:
+// chunked kernels for whole sequences (forward and backward) and a kernel for single tokens.
+//
+//   S_t = lambda S_{t-1} + k_t v_t^T   (d x d, fp32),   o_t = scale S_t^T q_t,   lambda = exp(g)
+//
+// Chunks of 128 tokens, i and j counting inside a chunk of m valid tokens, R the state that
+// the tokens before it leave:
+//   o_i = scale (lambda^(i+1) R^T q_i + sum_{j <= i} lambda^(i-j) (q_i . k_j) v_j)
+//   R  <- lambda^m R + sum_j lambda^(m-1-j) k_j v_j^T
+// so a chunk is four matrix products: P = Q K^T (weighted and masked), P V, Q R, and K^T V'
+// with V' the decayed values.  The state of a sequence stays in fp32 registers.
+//
+// Backward: with dS_t = lambda dS_{t+1} + scale q_t do_t^T,
+//   dq_t = scale S_t do_t,   dv_t = dS_t^T k_t,   dk_t = dS_t v_t,   dS_{-1} = lambda dS_0.
+// Each of the three is the forward's recurrence again with other tensors in its places:
+//   dq: (q, k, v) := (dO, V, K), state S^T;  dk: (V, dO, Q), dv: (K, Q, dO), time reversed.
+// So one kernel serves all four, and the backward's three passes share one launch.  Reversed,
+// the carried state is kept already decayed to the next token (index r = m - 1 - i):
+//   o_i = lambda^r R^T q_i + sum_{j >= i} lambda^(j-i) (..),  R <- lambda^m R + sum_j lambda^(j+1) k_j v_j^T
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace sigattn {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kChunk = 128;
+constexpr int kCols = 64;       // value columns of a work item
+constexpr int kSms = 148;       // B200
+constexpr int kMaxSorted = 512;  // batches up to this size are walked longest-first
+constexpr int kThreads = 512;
+constexpr int kWarpP = 4, kWarpV = 8, kWarpS = 12;  // first warps of the three warpgroups
+
+struct LinPass {
+  int q, k, v;     // which of the tensor maps stand in the places of q, k, v
+  int reverse;
+  float o1, o2;    // factors of Q R and of P V in the output
+  float vs;        // factor of V' (what the state accumulates)
+  __nv_bfloat16* out;
+  int64_t o_sb, o_sn, o_sh;
+  const float* init;    // state before the first chunk, nullptr: 0; element (row, col) of
+  int init_sr, init_sc;  // (b, h) at (b H + h) D D + row init_sr + col init_sc
+  float* fin;            // state after the last chunk [B, H, D, D], nullptr: not wanted
+  float* seg;            // [B, H, nseg, D, D]: see sigattn_linear_workspace_size
+};
+
+struct LinParams {
+  CUtensorMap map[4];
+  LinPass pass[3];
+  int npass, B, H, N, T, nseg, seg_chunks, nitems;
+  const int32_t* lengths;
+  const int32_t* cu;
+  const float* log_decay;
+  int* status;
+  unsigned long long wait_ns;
+};
+
+// log2 of the decay: log_decay above 0 counts as 0, and below -1e4 as -1e4 (lambda = 0 in
+// fp32 either way), so that 0 * log2(lambda) = 0 and lambda^0 = 1 for a decay of exp(-inf).
+__device__ __forceinline__ float clamped_decay(const LinParams& p, int h) {
+  return fmaxf(fminf(__ldg(p.log_decay + h), 0.0f), -1e4f);
+}
+
+struct Seq {
+  int n, row0, tma_b;  // tokens, first row in the tensors' token dimension, batch coordinate
+};
+
+// Lengths and offsets are device data: clamped, so that no value of theirs reaches outside
+// the tensors.
+__device__ __forceinline__ Seq sequence(const LinParams& p, int b) {
+  Seq s;
+  if (p.cu) {
+    s.row0 = max(0, min(__ldg(p.cu + b), p.T));
+    const int end = max(s.row0, min(__ldg(p.cu + b + 1), p.T));
+    s.n = min(end - s.row0, p.N);
+    s.tma_b = 0;
+  } else {
+    s.n = p.lengths ? max(0, min(__ldg(p.lengths + b), p.N)) : p.N;
+    s.row0 = 0;
+    s.tma_b = b;
+  }
+  return s;
+}
+
+struct Item {
+  int b, h, slice, pass, seg;
+  Seq s;
+  int c0, cn;  // its chunks [c0, c0 + cn)
+};
+
+// Work item w: sequences longest-first (order), then segment, head, pass and slice of value
+// columns, so that the items that read the same rows run side by side.
+template <int D>
+__device__ __forceinline__ Item decode(const LinParams& p, const uint16_t* order, int w) {
+  Item it;
+  it.slice = w % (D / kCols);
+  w /= D / kCols;
+  it.pass = w % p.npass;
+  w /= p.npass;
+  it.h = w % p.H;
+  w /= p.H;
+  it.seg = w % p.nseg;
+  w /= p.nseg;
+  it.b = p.B <= kMaxSorted ? order[w] : w;
+  it.s = sequence(p, it.b);
+  it.c0 = it.seg * p.seg_chunks;
+  const int chunks = (it.s.n + kChunk - 1) / kChunk;
+  it.cn = max(0, min(p.seg_chunks, chunks - it.c0));
+  return it;
+}
+
+// The j-th chunk of an item in its pass's direction, and its valid tokens.
+__device__ __forceinline__ int chunk_of(const Item& it, bool reverse, int j) {
+  return reverse ? it.c0 + it.cn - 1 - j : it.c0 + j;
+}
+__device__ __forceinline__ int valid_of(const Item& it, int c) {
+  return min(kChunk, it.s.n - c * kChunk);
+}
+
+template <int D, bool HILO>
+struct LinLayout {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBox = 128 * 128;            // 128 tokens x 64 bf16
+  static constexpr int kTile = kBoxes * kBox;       // a Q or K tile
+  static constexpr int kSt = D == 64 ? 3 : 2;       // stages of Q and K
+  static constexpr int kVs = D == 64 ? 4 : 3;       // stages of V
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + kSt * kTile;
+  static constexpr int kV = kK + kSt * kTile;
+  static constexpr int kVp = kV + kVs * kBox;       // V' (and its rounding error, HILO)
+  static constexpr int kR = kVp + (HILO ? 2 : 1) * kBox;  // bf16 state, D rows of 64
+  static constexpr int kBar = kR + D * 128;
+  // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2] u_full[2]
+  // u_empty[2] vp_full r_full o_empty done
+  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 12;
+  static constexpr int kMisc = kBar + 8 * kNumBars;  // tmem base, abort, drain flags
+  static constexpr int kOrder = kMisc + 16;
+  static constexpr int kBytes = kOrder + 2 * kMaxSorted;
+  static constexpr int kAlloc = kBytes + 1024;       // slack for 1024-byte alignment
+  // TMEM columns
+  static constexpr int kTS = 0;     // two S / P buffers of 128
+  static constexpr int kTO1 = 256;  // Q R
+  static constexpr int kTO2 = 320;  // P V
+  static constexpr int kTU = 384;   // two K^T V' buffers of 64
+};
+
+// OUT: the whole computation.  Otherwise only the state that each segment of a sequence
+// leaves from a zero start is computed, into pass.seg.
+// HILO: V' as the sum of two bf16 values (relative error 2^-18 instead of 2^-9), for the
+// calls that hand the fp32 state to the user; the outputs in bf16 do not need it.
+template <int D, bool OUT, bool HILO>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ LinParams p) {
+  using L = LinLayout<D, HILO>;
+  constexpr int ST = L::kSt, VS = L::kVs;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int warp = warp_id(), lane = lane_id();
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
+  uint64_t* qk_full = bars;
+  uint64_t* qk_empty = qk_full + ST;   // S, K^T V' and Q R of the chunk complete
+  uint64_t* v_full = qk_empty + ST;
+  uint64_t* pv_done = v_full + VS;     // P V of the chunk complete: outputs ready, V free
+  uint64_t* s_full = pv_done + VS;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* u_full = p_full + 2;       // K^T V' complete: U ready, V' free
+  uint64_t* u_empty = u_full + 2;
+  uint64_t* vp_full = u_empty + 2;
+  uint64_t* r_full = vp_full + 1;
+  uint64_t* o_empty = r_full + 1;
+  uint64_t* done = o_empty + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
+  uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::kOrder);
+  const WaitCtx wctx{p.status, p.wait_ns, abort_flag};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(qk_full + i, 1);
+      mbar_init(qk_empty + i, 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(v_full + i, 1);
+      mbar_init(pv_done + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+      mbar_init(u_full + i, 1);
+      mbar_init(u_empty + i, 4);
+    }
+    mbar_init(vp_full, 4);
+    mbar_init(r_full, 4);
+    mbar_init(o_empty, 4);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    *drain_flag = 0;
+    fence_barrier_init();
+  }
+  __syncwarp();
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  if (p.B <= kMaxSorted) {
+    // ranks by length, ties by index: every CTA derives the same order
+    int* len = reinterpret_cast<int*>(smem);  // before any tile arrives here
+    for (int b = threadIdx.x; b < p.B; b += kThreads) len[b] = sequence(p, b).n;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+      int rank = 0;
+      for (int x = 0; x < p.B; ++x) rank += len[x] > len[b] || (len[x] == len[b] && x < b);
+      order[rank] = static_cast<uint16_t>(b);
+    }
+    // the copies that overwrite len go through the async proxy
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int t = 0, tv = 0;  // chunks whose Q and K, whose V copies are issued
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int w = snake_item(k);
+        if (w >= p.nitems) break;
+        const Item it = decode<D>(p, order, w);
+        const LinPass& ps = p.pass[it.pass];
+        const CUtensorMap* mq = p.map + ps.q;
+        const CUtensorMap* mk = p.map + ps.k;
+        const CUtensorMap* mv = p.map + ps.v;
+        for (int j = 0; j < it.cn; ++j) {
+          const int s = t % ST, vs = tv % VS;
+          const int row = it.s.row0 + chunk_of(it, ps.reverse, j) * kChunk;
+          if (t >= ST && !(ok = mbar_wait(qk_empty + s, ((t / ST) - 1) & 1, wctx))) break;
+          mbar_arrive_expect_tx(qk_full + s, (OUT ? 2 : 1) * L::kTile);
+          for (int x = 0; x < L::kBoxes; ++x) {
+            tma_load_4d(smem + L::kK + s * L::kTile + x * L::kBox, mk, qk_full + s, x * 64, row,
+                        it.h, it.s.tma_b);
+            if (OUT)
+              tma_load_4d(smem + L::kQ + s * L::kTile + x * L::kBox, mq, qk_full + s, x * 64, row,
+                          it.h, it.s.tma_b);
+          }
+          ++t;
+          if (tv >= VS && !(ok = mbar_wait(pv_done + vs, ((tv / VS) - 1) & 1, wctx))) break;
+          mbar_arrive_expect_tx(v_full + vs, L::kBox);
+          tma_load_4d(smem + L::kV + vs * L::kBox, mv, v_full + vs, it.slice * kCols, row, it.h,
+                      it.s.tma_b);
+          ++tv;
+        }
+      }
+      if (*abort_flag) {
+        // Let the copies still in flight land before the CTA's shared memory goes away.
+        const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
+        for (int u = max(0, t - ST); u < t; ++u) mbar_wait(qk_full + u % ST, (u / ST) & 1, drain);
+        for (int u = max(0, tv - VS); u < tv; ++u) mbar_wait(v_full + u % VS, (u / VS) & 1, drain);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    // Four streams of products, each in chunk order; whichever has its operands goes next.
+    // The tensor pipe runs in issue order, so a buffer may be overwritten by a product that
+    // is issued after the last one that reads it.
+    constexpr uint32_t kHi = sw128_desc_hi(1024);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, kCols, true);
+    constexpr uint32_t idesc_u = idesc_bf16_f32(128, kCols, true, true);
+    int total = 0;
+    for (int k = 0;; ++k) {
+      const int w = snake_item(k);
+      if (w >= p.nitems) break;
+      total += decode<D>(p, order, w).cn;
+    }
+    auto ready = [](uint64_t* bar, int phase) {
+      return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)) != 0;
+    };
+    int ts = 0, tu = 0, to = 0, tp = 0;  // next chunk of each stream
+    long long t0 = clock64();
+    const long long limit = static_cast<long long>(p.wait_ns) * 2;
+    while ((OUT ? tp : tu) < total) {
+      bool progress = false;
+      if (OUT && tp < to && ready(p_full + (tp & 1), tp >> 1)) {
+        // O2 = P V (P from TMEM, 16 keys in 8 columns)
+        tc_fence_after();
+        const uint32_t v_base = smem_u32(smem + L::kV + (tp % VS) * L::kBox);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts_lh_w(tmem + L::kTO2, tmem + L::kTS + (tp & 1) * 128 + kk * 8,
+                      sw128_desc_lo(v_base + kk * 2048, L::kBox), kHi, idesc_o, kk > 0);
+        mma_commit_w(pv_done + tp % VS);
+        ++tp;
+        progress = true;
+      }
+      if (OUT && to < tu && ready(r_full, to) && (to == 0 || ready(o_empty, to - 1))) {
+        // O1 = Q R; with S and U of the chunk issued before, Q and K are free after it
+        tc_fence_after();
+        const uint32_t q_base = smem_u32(smem + L::kQ + (to % ST) * L::kTile);
+        const uint32_t r_base = smem_u32(smem + L::kR);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss_lh_w(tmem + L::kTO1,
+                      sw128_desc_lo(q_base + (kk >> 2) * L::kBox + (kk & 3) * 32, 16),
+                      sw128_desc_lo(r_base + kk * 2048, L::kBox), kHi, idesc_o, kk > 0);
+        mma_commit_w(qk_empty + to % ST);
+        ++to;
+        progress = true;
+      }
+      if (tu < (OUT ? ts : total) && ready(vp_full, tu) &&
+          (tu < 2 || ready(u_empty + (tu & 1), (tu >> 1) - 1)) &&
+          (OUT || ready(qk_full + tu % ST, tu / ST))) {
+        // U = K^T V'.  A holds the K columns as rows: 128 for d = 128; for d = 64 the chunk
+        // stride of 0 gives them twice, lanes 64-127 a copy of lanes 0-63.
+        tc_fence_after();
+        const uint32_t k_base = smem_u32(smem + L::kK + (tu % ST) * L::kTile);
+        const uint32_t v_base = smem_u32(smem + L::kVp);
+#pragma unroll
+        for (int x = 0; x < (HILO ? 2 : 1); ++x)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss_lh_w(tmem + L::kTU + (tu & 1) * 64,
+                        sw128_desc_lo(k_base + kk * 2048, D == 128 ? L::kBox : 0),
+                        sw128_desc_lo(v_base + x * L::kBox + kk * 2048, L::kBox), kHi, idesc_u,
+                        x + kk > 0);
+        mma_commit_w(u_full + (tu & 1));
+        if (!OUT) {
+          mma_commit_w(qk_empty + tu % ST);
+          mma_commit_w(pv_done + tu % VS);
+        }
+        ++tu;
+        progress = true;
+      }
+      if (OUT && ts < total && ts < tp + 2 && ready(qk_full + ts % ST, ts / ST)) {
+        // S = Q K^T
+        tc_fence_after();
+        const uint32_t q_base = smem_u32(smem + L::kQ + (ts % ST) * L::kTile);
+        const uint32_t k_base = smem_u32(smem + L::kK + (ts % ST) * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
+          mma_ss_lh_w(tmem + L::kTS + (ts & 1) * 128, sw128_desc_lo(q_base + off, 16),
+                      sw128_desc_lo(k_base + off, 16), kHi, idesc_s, kk > 0);
+        }
+        mma_commit_w(s_full + (ts & 1));
+        ++ts;
+        progress = true;
+      }
+      if (progress) {
+        t0 = clock64();
+      } else {
+        const bool late = __any_sync(0xFFFFFFFFu, clock64() - t0 > limit);
+        if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) {
+          if (lane == 0 && late) atomicOr(p.status, kStatusTimeout);
+          *abort_flag = 1;
+          break;
+        }
+      }
+    }
+    // every MMA complete before the TMEM is released (also after an abort)
+    mma_commit_w(done);
+    const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
+    mbar_wait_w(done, 0, drain);
+  } else if (warp < kWarpP) {
+    // ---------------------------------------------------------------- zero rows
+    // Rows behind a padded sequence, within the item's segment, are written as 0.
+    if (OUT && !p.cu) {
+      for (int k = 0;; ++k) {
+        const int w = snake_item(k);
+        if (w >= p.nitems) break;
+        const Item it = decode<D>(p, order, w);
+        const LinPass& ps = p.pass[it.pass];
+        const int lo = it.c0 * kChunk;
+        const int hi = it.seg == p.nseg - 1 ? p.N : min(p.N, lo + p.seg_chunks * kChunk);
+        __nv_bfloat16* out = ps.out + it.b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols;
+        for (int r = max(lo, it.s.n) + (warp - 2) * 4 + lane / 8; r < hi; r += 8)
+          *reinterpret_cast<uint4*>(out + r * ps.o_sn + (lane % 8) * 8) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  } else if (warp < kWarpV) {
+    // ---------------------------------------------------------------- P = decayed, masked S
+    if (OUT) {
+      const int wq = warp & 3, i = wq * 32 + lane;
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+      int t = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int w = snake_item(k);
+        if (w >= p.nitems) break;
+        const Item it = decode<D>(p, order, w);
+        const bool rev = p.pass[it.pass].reverse != 0;
+        const float l2 = clamped_decay(p, it.h) * kLog2e;
+        for (int j = 0; j < it.cn; ++j, ++t) {
+          const int m = valid_of(it, chunk_of(it, rev, j));
+          const uint32_t sb = t_lane + L::kTS + (t & 1) * 128;
+          if (!(ok = mbar_wait_w(s_full + (t & 1), (t >> 1) & 1, wctx))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int blk = 0; blk < 4; ++blk) {
+            uint32_t pk[16];
+            if (rev ? blk < wq : blk > wq) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) pk[c] = 0u;
+            } else {
+              uint32_t sr[32];
+              tmem_ld32(sb + blk * 32, sr);
+              tmem_wait_ld();
+              // lambda^|i - j|: j = 32 blk + c, so l2 |i - j| = x0 -+ l2 c
+              const int at = blk * 32 - i;  // j - i of the block's first column
+              const float x0 = l2 * static_cast<float>(rev ? at : -at), dx = rev ? l2 : -l2;
+              float f[32];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const bool keep = rev ? (at + c >= 0 && blk * 32 + c < m) : at + c <= 0;
+                const float x = ex2_approx(fmaf(dx, static_cast<float>(c), x0));
+                f[c] = keep ? __uint_as_float(sr[c]) * x : 0.0f;
+              }
+#pragma unroll
+              for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(f[2 * c], f[2 * c + 1]);
+            }
+            tmem_st16(sb + blk * 16, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + (t & 1));
+        }
+      }
+    }
+  } else if (warp < kWarpS) {
+    // ---------------------------------------------------------------- V' and the outputs
+    const int wq = warp & 3, tid = threadIdx.x - kWarpV * 32;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const int i = wq * 32 + lane;
+    int t = 0;
+    bool ok = true;
+    // the chunk whose outputs are still to be written
+    __nv_bfloat16* o_row = nullptr;
+    float o_f1 = 0.0f, o_f2 = 0.0f;
+    auto write_out = [&](int to) -> bool {
+      if (!mbar_wait_w(pv_done + to % VS, (to / VS) & 1, wctx)) return false;
+      tc_fence_after();
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t a[16], b[16];
+        tmem_ld16(t_lane + L::kTO1 + c * 16, a);
+        tmem_ld16(t_lane + L::kTO2 + c * 16, b);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          pk[c * 8 + x] = pack_bf16x2(
+              fmaf(o_f1, __uint_as_float(a[2 * x]), o_f2 * __uint_as_float(b[2 * x])),
+              fmaf(o_f1, __uint_as_float(a[2 * x + 1]), o_f2 * __uint_as_float(b[2 * x + 1])));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_empty);
+      if (o_row) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          reinterpret_cast<uint4*>(o_row)[c] =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+      }
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      const int w = snake_item(k);
+      if (w >= p.nitems) break;
+      const Item it = decode<D>(p, order, w);
+      const LinPass& ps = p.pass[it.pass];
+      const bool rev = ps.reverse != 0;
+      const float l2 = clamped_decay(p, it.h) * kLog2e;
+      for (int j = 0; j < it.cn; ++j, ++t) {
+        const int c = chunk_of(it, rev, j), m = valid_of(it, c);
+        const int vs = t % VS, s = t % ST;
+        if (!(ok = mbar_wait_w(v_full + vs, (t / VS) & 1, wctx))) break;
+        if (m < kChunk && !(ok = mbar_wait_w(qk_full + s, (t / ST) & 1, wctx))) break;
+        if (t > 0 && !(ok = mbar_wait_w(u_full + ((t - 1) & 1), ((t - 1) >> 1) & 1, wctx))) break;
+        uint8_t* v = smem + L::kV + vs * L::kBox;
+        uint8_t* vp = smem + L::kVp;
+        // 16 bytes a step, at the address they have in the swizzled tile: its row is what
+        // counts
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int off = (tid + x * 128) * 16, row = off / 128;
+          uint4 in = *reinterpret_cast<const uint4*>(v + off);
+          const float f =
+              ps.vs * ex2_approx(l2 * static_cast<float>(rev ? row + 1 : m - 1 - row));
+          uint32_t hi[4], lo[4];
+          const uint32_t wds[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float a = __uint_as_float(wds[y] << 16) * f;
+            const float b = __uint_as_float(wds[y] & 0xFFFF0000u) * f;
+            hi[y] = pack_bf16x2(a, b);
+            if (HILO)
+              lo[y] = pack_bf16x2(a - __uint_as_float(hi[y] << 16),
+                                  b - __uint_as_float(hi[y] & 0xFFFF0000u));
+          }
+          if (row >= m) {
+            // behind the sequence: whatever these rows hold (NaN among it) must not reach
+            // the products over tokens, V' and V as factors of 0 no more than K
+            for (int y = 0; y < 4; ++y) hi[y] = lo[y] = 0u;
+            *reinterpret_cast<uint4*>(v + off) = make_uint4(0u, 0u, 0u, 0u);
+            for (int y = 0; y < L::kBoxes; ++y)
+              *reinterpret_cast<uint4*>(smem + L::kK + s * L::kTile + y * L::kBox + off) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          *reinterpret_cast<uint4*>(vp + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if (HILO)
+            *reinterpret_cast<uint4*>(vp + L::kBox + off) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vp_full);
+        if (OUT) {
+          if (t > 0 && !(ok = write_out(t - 1))) break;
+          o_row = i < m ? ps.out + it.s.tma_b * ps.o_sb +
+                              (it.s.row0 + c * kChunk + i) * ps.o_sn + it.h * ps.o_sh +
+                              it.slice * kCols
+                        : nullptr;
+          o_f1 = ps.o1 * ex2_approx(l2 * static_cast<float>(rev ? m - 1 - i : i + 1));
+          o_f2 = ps.o2;
+        }
+      }
+    }
+    if (OUT && ok && t > 0) write_out(t - 1);
+  } else {
+    // ---------------------------------------------------------------- the state
+    // d = 128: a thread holds one row of the state, 64 columns; d = 64: half a row, the
+    // second half from the copy of the row in lanes 64-127 of U.
+    constexpr int kHold = D == 128 ? 64 : 32;
+    const int wq = warp & 3;
+    const int row = D == 128 ? wq * 32 + lane : (wq & 1) * 32 + lane;
+    const int col0 = D == 128 ? 0 : (wq >> 1) * 32;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16) + L::kTU + col0;
+    float r[kHold];
+    int t = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int w = snake_item(k);
+      if (w >= p.nitems) break;
+      const Item it = decode<D>(p, order, w);
+      const LinPass& ps = p.pass[it.pass];
+      const bool rev = ps.reverse != 0;
+      const int64_t bh = static_cast<int64_t>(it.b) * p.H + it.h;
+      float* seg = ps.seg + ((bh * p.nseg + it.seg) * D + row) * D + it.slice * kCols + col0;
+      // exp in 64 bits: the factor is applied once a chunk, so its error adds up
+      const double g = static_cast<double>(clamped_decay(p, it.h));
+      const float full = static_cast<float>(exp(g * kChunk));
+      if (OUT && p.nseg > 1) {
+        if (it.cn > 0)
+#pragma unroll
+          for (int c = 0; c < kHold; c += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(seg + c);
+            r[c] = x.x, r[c + 1] = x.y, r[c + 2] = x.z, r[c + 3] = x.w;
+          }
+      } else if (OUT && ps.init) {
+        const float* at = ps.init + bh * D * D + row * ps.init_sr +
+                          static_cast<int64_t>(it.slice * kCols + col0) * ps.init_sc;
+#pragma unroll
+        for (int c = 0; c < kHold; ++c) r[c] = at[c * ps.init_sc];
+      } else {
+#pragma unroll
+        for (int c = 0; c < kHold; ++c) r[c] = 0.0f;
+      }
+      for (int j = 0; j < it.cn; ++j, ++t) {
+        const int m = valid_of(it, chunk_of(it, rev, j));
+        if (OUT) {
+          // the state as the B operand of Q R: row by row, 128 swizzled bytes each
+          if (t > 0 && !(ok = mbar_wait_w(qk_empty + (t - 1) % ST, ((t - 1) / ST) & 1, wctx)))
+            break;
+          uint8_t* dst = smem + L::kR + row * 128;
+#pragma unroll
+          for (int c = 0; c < kHold / 8; ++c)
+            *reinterpret_cast<uint4*>(dst + (((col0 / 8 + c) ^ (row & 7)) << 4)) =
+                make_uint4(pack_bf16x2(r[8 * c], r[8 * c + 1]),
+                           pack_bf16x2(r[8 * c + 2], r[8 * c + 3]),
+                           pack_bf16x2(r[8 * c + 4], r[8 * c + 5]),
+                           pack_bf16x2(r[8 * c + 6], r[8 * c + 7]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(r_full);
+        }
+        if (!(ok = mbar_wait_w(u_full + (t & 1), (t >> 1) & 1, wctx))) break;
+        tc_fence_after();
+        const float f = m == kChunk ? full : static_cast<float>(exp(g * m));
+#pragma unroll
+        for (int c = 0; c < kHold; c += 32) {
+          uint32_t u[32];
+          tmem_ld32(t_lane + (t & 1) * 64 + c, u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[c + x] = fmaf(f, r[c + x], __uint_as_float(u[x]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty + (t & 1));
+      }
+      float* dst = !OUT ? (it.cn > 0 ? seg : nullptr)
+                   : (p.nseg == 1 && ps.fin)
+                       ? ps.fin + (bh * D + row) * D + it.slice * kCols + col0
+                       : nullptr;
+      if (ok && dst) {
+#pragma unroll
+        for (int c = 0; c < kHold; c += 4)
+          *reinterpret_cast<float4*>(dst + c) = make_float4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The states that the segments start from, in place of what each leaves from a zero start,
+// and the final state.  One thread per state element and (b, h, pass); four columns each.
+template <int D>
+__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LinParams p) {
+  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
+  const LinPass& ps = p.pass[blockIdx.z];
+  const int n = sequence(p, b).n, rows = p.seg_chunks * kChunk;
+  const int segs = (n + rows - 1) / rows;
+  const double g = static_cast<double>(clamped_decay(p, h));
+  const float full = static_cast<float>(exp(g * rows));
+  const float part = static_cast<float>(exp(g * (n - (segs - 1) * rows)));  // the last segment
+  float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (ps.init) {
+    const float* at = ps.init + static_cast<int64_t>(bh) * D * D + (e / D) * ps.init_sr +
+                      (e % D) * ps.init_sc;
+    r = make_float4(at[0], at[ps.init_sc], at[2 * ps.init_sc], at[3 * ps.init_sc]);
+  }
+  float* seg = ps.seg + static_cast<int64_t>(bh) * p.nseg * D * D + e;
+  for (int x = 0; x < segs; ++x) {
+    const int s = ps.reverse ? segs - 1 - x : x;
+    float4* at = reinterpret_cast<float4*>(seg + static_cast<int64_t>(s) * D * D);
+    const float4 u = *at;
+    *at = r;
+    const float f = s == segs - 1 ? part : full;
+    r = make_float4(fmaf(f, r.x, u.x), fmaf(f, r.y, u.y), fmaf(f, r.z, u.z), fmaf(f, r.w, u.w));
+  }
+  if (ps.fin) *reinterpret_cast<float4*>(ps.fin + static_cast<int64_t>(bh) * D * D + e) = r;
+}
+
+// ------------------------------------------------------------------------------------
+// Single tokens: one pass over the state, read, updated, written, and contracted with q.
+// A CTA takes 32 columns of one (b, h): 8 lanes of 16 bytes cover a row's 128 bytes, a warp
+// four rows, and every load of a thread (d / 32 of them) is issued before the first is used.
+// ------------------------------------------------------------------------------------
+struct StepParams {
+  int H;
+  const int32_t* lengths;
+  const float* log_decay;
+  float scale;
+  const __nv_bfloat16 *q, *k, *v;
+  __nv_bfloat16* o;
+  int64_t q_sb, q_sh, k_sb, k_sh, v_sb, v_sh, o_sb, o_sh;
+  const float* in;
+  float* out;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) k_linear_step(const StepParams p) {
+  __shared__ float sums[8][32];
+  const int bh = blockIdx.x / (D / 32), c0 = (blockIdx.x % (D / 32)) * 32;
+  const int b = bh / p.H, h = bh % p.H;
+  const int col = c0 + (threadIdx.x % 8) * 4, row0 = threadIdx.x / 8;
+  const int64_t base = static_cast<int64_t>(bh) * D * D + col;
+  float4 s[D / 32];
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x)
+    s[x] = *reinterpret_cast<const float4*>(p.in + base + (row0 + 32 * x) * D);
+  const bool active = !p.lengths || __ldg(p.lengths + b) > 0;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (active) {
+    const float f = expf(fminf(__ldg(p.log_decay + h), 0.0f));
+    const __nv_bfloat16* v = p.v + b * p.v_sb + h * p.v_sh + col;
+    const float v0 = __bfloat162float(v[0]), v1 = __bfloat162float(v[1]),
+                v2 = __bfloat162float(v[2]), v3 = __bfloat162float(v[3]);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+      const int row = row0 + 32 * x;
+      const float k = __bfloat162float(p.k[b * p.k_sb + h * p.k_sh + row]);
+      const float q = __bfloat162float(p.q[b * p.q_sb + h * p.q_sh + row]);
+      s[x] = make_float4(fmaf(f, s[x].x, k * v0), fmaf(f, s[x].y, k * v1),
+                         fmaf(f, s[x].z, k * v2), fmaf(f, s[x].w, k * v3));
+      o = make_float4(fmaf(q, s[x].x, o.x), fmaf(q, s[x].y, o.y), fmaf(q, s[x].z, o.z),
+                      fmaf(q, s[x].w, o.w));
+    }
+  }
+  if (active || p.out != p.in) {
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+      *reinterpret_cast<float4*>(p.out + base + (row0 + 32 * x) * D) = s[x];
+  }
+#pragma unroll
+  for (int m = 8; m <= 16; m <<= 1) {
+    o.x += __shfl_xor_sync(0xFFFFFFFFu, o.x, m);
+    o.y += __shfl_xor_sync(0xFFFFFFFFu, o.y, m);
+    o.z += __shfl_xor_sync(0xFFFFFFFFu, o.z, m);
+    o.w += __shfl_xor_sync(0xFFFFFFFFu, o.w, m);
+  }
+  if (threadIdx.x % 32 < 8)
+    *reinterpret_cast<float4*>(&sums[threadIdx.x / 32][(threadIdx.x % 8) * 4]) = o;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    float a = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) a += sums[x][threadIdx.x];
+    p.o[b * p.o_sb + h * p.o_sh + c0 + threadIdx.x] = __float2bfloat16(active ? p.scale * a : 0.0f);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Launches
+// ------------------------------------------------------------------------------------
+// How a sequence is cut when there are fewer (pass, batch, head, slice) items than SMs: into
+// segments whose states are computed first, from their keys and values alone, and joined.
+void segments(int npass, int B, int N, int H, int d, int* nseg, int* seg_chunks) {
+  const int64_t items = static_cast<int64_t>(npass) * B * H * (d / kCols);
+  const int chunks = (N + kChunk - 1) / kChunk;
+  int want = items >= kSms ? 1 : static_cast<int>(kSms / items);
+  want = std::max(1, std::min(want, chunks / 4));
+  *seg_chunks = (chunks + want - 1) / want;
+  *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
+}
+
+template <int D, bool OUT, bool HILO>
+int launch_one(const LinParams& p, cudaStream_t stream) {
+  using L = LinLayout<D, HILO>;
+  static_assert(L::kAlloc <= 227 * 1024, "shared memory");
+  auto kern = linear_kernel<D, OUT, HILO>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return cuda_status(e);
+  kern<<<std::min(p.nitems, kSms), kThreads, L::kAlloc, stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+int launch(const LinParams& p, cudaStream_t stream) {
+  bool fin = false;
+  for (int i = 0; i < p.npass; ++i) fin = fin || p.pass[i].fin;
+  if (p.nseg == 1)
+    return fin ? launch_one<D, true, true>(p, stream) : launch_one<D, true, false>(p, stream);
+  int rc = fin ? launch_one<D, false, true>(p, stream) : launch_one<D, false, false>(p, stream);
+  if (rc != SIGATTN_OK) return rc;
+  k_linear_join<D><<<dim3(D * D / 1024, p.B * p.H, p.npass), 256, 0, stream>>>(p);
+  if ((rc = cuda_status(cudaGetLastError())) != SIGATTN_OK) return rc;
+  return launch_one<D, true, false>(p, stream);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int check_tensor(const void* ptr, const int64_t* strides, int rows, TensorDesc* t) {
+  if (!ptr || !strides) return SIGATTN_ERR_INVALID;
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] < 0) return SIGATTN_ERR_INVALID;
+  if (!aligned16(ptr)) return SIGATTN_ERR_ALIGNMENT;
+  for (int i = 0; i < 3; ++i)
+    if (strides[i] % 8 != 0) return SIGATTN_ERR_ALIGNMENT;
+  *t = TensorDesc{ptr, strides[0], strides[1], strides[2], rows};
+  return SIGATTN_OK;
+}
+
+int check_sizes(int B, int N, int64_t T, int H, int d, bool packed) {
+  if (B < 1 || N < 1 || H < 1 || (packed && T < 1)) return SIGATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return SIGATTN_ERR_UNSUPPORTED;
+  // row indices, item counts (six items per batch, head and segment at most, fewer than
+  // 148 segments where items are few) and the join's grid stay below their limits
+  if (N > 0x7FFFFF00 || (packed && T > 0x7FFFFF00)) return SIGATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * H > 0x0FFFFFFF) return SIGATTN_ERR_UNSUPPORTED;
+  return SIGATTN_OK;
+}
+
+// Fills what the passes share; the tensor maps are those of t[0..n).
+int fill(LinParams* p, int npass, int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+         const int32_t* cu, const float* log_decay, const TensorDesc* t, int n) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SIGATTN_ERR_NO_DEVICE;
+  }
+  int rc;
+  if ((rc = status_ptr(&p->status)) != SIGATTN_OK) return rc;
+  for (int i = 0; i < n; ++i)
+    if ((rc = make_tmap_bf16(&p->map[i], t[i], cu ? 1 : B, H, d)) != SIGATTN_OK) return rc;
+  p->npass = npass;
+  p->B = B;
+  p->H = H;
+  p->N = N;
+  p->T = static_cast<int>(T);
+  segments(npass, B, N, H, d, &p->nseg, &p->seg_chunks);
+  p->nitems = npass * B * p->nseg * H * (d / kCols);
+  p->lengths = lengths;
+  p->cu = cu;
+  p->log_decay = log_decay;
+  p->wait_ns = wait_limit_ns();
+  return SIGATTN_OK;
+}
+
+void set_out(LinPass* ps, const TensorDesc& o) {
+  ps->out = static_cast<__nv_bfloat16*>(const_cast<void*>(o.ptr));
+  ps->o_sb = o.sb;
+  ps->o_sn = o.sn;
+  ps->o_sh = o.sh;
+}
+
+size_t workspace_bytes_of(int npass, int B, int N, int H, int d) {
+  int nseg, seg_chunks;
+  segments(npass, B, N, H, d, &nseg, &seg_chunks);
+  return nseg == 1 ? 0 : sizeof(float) * npass * B * H * nseg * d * d;
+}
+
+}  // namespace
+}  // namespace sigattn
+
+using namespace sigattn;
+
+extern "C" int sigattn_linear_workspace_size(int B, int N, int H, int d, int backward,
+                                             size_t* bytes) {
+  if (!bytes || (backward != 0 && backward != 1)) return SIGATTN_ERR_INVALID;
+  const int rc = check_sizes(B, N, 1, H, d, false);
+  if (rc != SIGATTN_OK) return rc;
+  *bytes = workspace_bytes_of(backward ? 3 : 1, B, N, H, d);
+  return SIGATTN_OK;
+}
+
+extern "C" int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                  const int32_t* cu_seqlens, const float* log_decay, float scale,
+                                  const void* q, const int64_t q_strides[3], const void* k,
+                                  const int64_t k_strides[3], const void* v,
+                                  const int64_t v_strides[3], const float* state, void* o,
+                                  const int64_t o_strides[3], float* final_state, void* workspace,
+                                  size_t workspace_bytes, sigattn_stream s) {
+  const bool packed = cu_seqlens != nullptr;
+  int rc = check_sizes(B, N, T, H, d, packed);
+  if (rc != SIGATTN_OK) return rc;
+  if (!log_decay || !std::isfinite(scale) || (packed && lengths)) return SIGATTN_ERR_INVALID;
+  const int rows = packed ? static_cast<int>(T) : N;
+  TensorDesc t[3], to;
+  if ((rc = check_tensor(q, q_strides, rows, &t[0])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(k, k_strides, rows, &t[1])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(v, v_strides, rows, &t[2])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(o, o_strides, rows, &to)) != SIGATTN_OK) return rc;
+  const size_t need = workspace_bytes_of(1, B, N, H, d);
+  if (need && (!workspace || workspace_bytes < need)) return SIGATTN_ERR_INVALID;
+  if (!aligned16(state) || !aligned16(final_state) || !aligned16(workspace))
+    return SIGATTN_ERR_ALIGNMENT;
+  LinParams p;
+  std::memset(&p, 0, sizeof(p));
+  if ((rc = fill(&p, 1, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 3)) != SIGATTN_OK)
+    return rc;
+  LinPass& ps = p.pass[0];
+  ps.q = 0, ps.k = 1, ps.v = 2;
+  ps.o1 = ps.o2 = scale;
+  ps.vs = 1.0f;
+  set_out(&ps, to);
+  ps.init = state;
+  ps.init_sr = d;
+  ps.init_sc = 1;
+  ps.fin = final_state;
+  ps.seg = static_cast<float*>(workspace);
+  const cudaStream_t stream = static_cast<cudaStream_t>(s);
+  return d == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                  const int32_t* cu_seqlens, const float* log_decay, float scale,
+                                  const void* q, const int64_t q_strides[3], const void* k,
+                                  const int64_t k_strides[3], const void* v,
+                                  const int64_t v_strides[3], const void* dout,
+                                  const int64_t do_strides[3], const float* state,
+                                  const float* dfinal_state, void* dq, const int64_t dq_strides[3],
+                                  void* dk, const int64_t dk_strides[3], void* dv,
+                                  const int64_t dv_strides[3], float* dstate, void* workspace,
+                                  size_t workspace_bytes, sigattn_stream s) {
+  const bool packed = cu_seqlens != nullptr;
+  int rc = check_sizes(B, N, T, H, d, packed);
+  if (rc != SIGATTN_OK) return rc;
+  if (!log_decay || !std::isfinite(scale) || (packed && lengths)) return SIGATTN_ERR_INVALID;
+  const int rows = packed ? static_cast<int>(T) : N;
+  TensorDesc t[4], tdq, tdk, tdv;
+  if ((rc = check_tensor(q, q_strides, rows, &t[0])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(k, k_strides, rows, &t[1])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(v, v_strides, rows, &t[2])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dout, do_strides, rows, &t[3])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dq, dq_strides, rows, &tdq)) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dk, dk_strides, rows, &tdk)) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dv, dv_strides, rows, &tdv)) != SIGATTN_OK) return rc;
+  const size_t need = workspace_bytes_of(3, B, N, H, d);
+  if (need && (!workspace || workspace_bytes < need)) return SIGATTN_ERR_INVALID;
+  if (!aligned16(state) || !aligned16(dfinal_state) || !aligned16(dstate) || !aligned16(workspace))
+    return SIGATTN_ERR_ALIGNMENT;
+  LinParams p;
+  std::memset(&p, 0, sizeof(p));
+  if ((rc = fill(&p, 3, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 4)) != SIGATTN_OK)
+    return rc;
+  const size_t part = need / 3 / sizeof(float);
+  for (int i = 0; i < 3; ++i)
+    p.pass[i].seg = workspace ? static_cast<float*>(workspace) + i * part : nullptr;
+  // dq_t = scale S_t do_t: the forward's direction over (dO, V, K), state transposed
+  LinPass& a = p.pass[0];
+  a.q = 3, a.k = 2, a.v = 1;
+  a.o1 = a.o2 = scale;
+  a.vs = 1.0f;
+  set_out(&a, tdq);
+  a.init = state;
+  a.init_sr = 1;
+  a.init_sc = d;
+  // dk_t = dS_t v_t: reversed over (V, dO, Q), state dS^T
+  LinPass& b = p.pass[1];
+  b.q = 2, b.k = 3, b.v = 0;
+  b.reverse = 1;
+  b.o1 = 1.0f;
+  b.o2 = b.vs = scale;
+  set_out(&b, tdk);
+  b.init = dfinal_state;
+  b.init_sr = 1;
+  b.init_sc = d;
+  // dv_t = dS_t^T k_t: reversed over (K, Q, dO), state dS
+  LinPass& c = p.pass[2];
+  c.q = 1, c.k = 0, c.v = 3;
+  c.reverse = 1;
+  c.o1 = 1.0f;
+  c.o2 = c.vs = scale;
+  set_out(&c, tdv);
+  c.init = dfinal_state;
+  c.init_sr = d;
+  c.init_sc = 1;
+  c.fin = dstate;
+  const cudaStream_t stream = static_cast<cudaStream_t>(s);
+  return d == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+extern "C" int sigattn_linear_step(int B, int H, int d, const int32_t* lengths,
+                                   const float* log_decay, float scale, const void* q,
+                                   const int64_t q_strides[2], const void* k,
+                                   const int64_t k_strides[2], const void* v,
+                                   const int64_t v_strides[2], const float* state,
+                                   float* state_out, void* o, const int64_t o_strides[2],
+                                   sigattn_stream s) {
+  if (B < 1 || H < 1 || !log_decay || !std::isfinite(scale)) return SIGATTN_ERR_INVALID;
+  if (!q || !k || !v || !o || !state || !state_out) return SIGATTN_ERR_INVALID;
+  if (!q_strides || !k_strides || !v_strides || !o_strides) return SIGATTN_ERR_INVALID;
+  for (int i = 0; i < 2; ++i)
+    if (q_strides[i] < 0 || k_strides[i] < 0 || v_strides[i] < 0 || o_strides[i] < 0)
+      return SIGATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return SIGATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * H * (d / 32) > 0x7FFFFFFF) return SIGATTN_ERR_UNSUPPORTED;
+  if (!aligned16(state) || !aligned16(state_out)) return SIGATTN_ERR_ALIGNMENT;
+  const auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
+  StepParams p{H,
+               lengths,
+               log_decay,
+               scale,
+               bf(q),
+               bf(k),
+               bf(v),
+               static_cast<__nv_bfloat16*>(o),
+               q_strides[0],
+               q_strides[1],
+               k_strides[0],
+               k_strides[1],
+               v_strides[0],
+               v_strides[1],
+               o_strides[0],
+               o_strides[1],
+               state,
+               state_out};
+  const unsigned grid = static_cast<unsigned>(B) * H * (d / 32);
+  const cudaStream_t stream = static_cast<cudaStream_t>(s);
+  if (d == 64)
+    k_linear_step<64><<<grid, 256, 0, stream>>>(p);
+  else
+    k_linear_step<128><<<grid, 256, 0, stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
