@@ -221,7 +221,8 @@ def _run_qk_bwd(st, case):
     lengths = st["lengths"] if case["layout"] == "padded" else None
     if own:
         from padded_variable_length_b200 import binding as Bd
-        return Bd.qk_norm_rope_bwd(st["q"], st["k"], st["dyq"], st["dyk"], st["wq"], st["wk"], eps=1e-6, lengths=lengths, **st["rope"])
+        dq, dk, dwq, dwk = Bd.qk_norm_rope_bwd(st["q"], st["k"], st["dyq"], st["dyk"], st["wq"], st["wk"], eps=1e-6, lengths=lengths, **st["rope"])
+        return dq, dwq, dk, dwk
     cs = _cos_sin(case, st["rope"])
     return _qk_grad(st, "q", cs, case, lengths) + _qk_grad(st, "k", cs, case, lengths)
 
