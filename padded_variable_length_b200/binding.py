@@ -7,6 +7,7 @@ the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional
@@ -436,112 +437,157 @@ def bwd_fused(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, ls
 # --------------------------------------------------------------------------------------
 # Norm and rotation of queries and keys; linear attention
 # --------------------------------------------------------------------------------------
-def _tensor(t, name: str, dim=(3, 4)) -> torch.Tensor:
-    """A bf16 CUDA tensor on the current device, d contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() not in dim:
-        raise ValueError(f"{name} must be a bf16 tensor of {' or '.join(map(str, dim))} dimensions")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _on_device(t, name)
+# On a few tokens the checks here take longer than the kernels, so what follows from shapes
+# and strides alone is worked out once for each combination and looked up after that.
+_MEMO_ENTRIES = 4096
+_layouts: dict = {}
+_qk_shapes: dict = {}
+_section_arrays: dict = {}
 
 
-def _on_device(t: torch.Tensor, name: str) -> torch.Tensor:
-    """Kernels run on the current device: a tensor that lives elsewhere is refused."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _remember(memo: dict, key, value):
+    if len(memo) >= _MEMO_ENTRIES:
+        memo.clear()
+    memo[key] = value
+    return value
+
+
+class _Layout:
+    """Of a tensor's shape and strides: the strides the library takes, (batch, token, head)
+    and for single tokens (batch, head), and whether entries share memory.  A dimension of
+    one entry is never stepped over: 0 is passed, whatever its stride is."""
+    __slots__ = ("shape", "strides", "strides2", "expanded")
+
+    def __init__(self, shape, stride):
+        if stride[-1] != 1 and shape[-1] != 1:
+            raise ValueError("the last dimension must be contiguous")
+        s = [st if n > 1 else 0 for st, n in zip(stride, shape)][:-1]
+        self.shape = tuple(shape)
+        self.strides = _I64x3(*([0] * (3 - len(s)) + s))
+        self.strides2 = _I64x2(*s[-2:])
+        self.expanded = any(st == 0 and n > 1 for st, n in zip(stride, shape))
+
+
+_NO_STRIDES = _I64x3(0, 0, 0)
+
+
+def _here() -> int:
+    """The current device, on which the kernels run (-2, no tensor's device, without a GPU)."""
+    try:
+        return _current_device() if _current_device is not None else torch.cuda.current_device()
+    except RuntimeError:
+        return -2
+
+
+def _tensor(t, name: str, dev: int, dims=(3, 4)) -> _Layout:
+    """Layout of a bf16 tensor on device ``dev``, the last dimension contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() not in dims:
+        raise ValueError(f"{name} must be a bf16 tensor of {' or '.join(map(str, dims))} dimensions")
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
-    return t
+    key = (t.shape, t.stride())
+    lay = _layouts.get(key)
+    return lay if lay is not None else _remember(_layouts, key, _Layout(*key))
 
 
-def _small(t, name: str, dtype, shape) -> Optional[int]:
+def _small(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     """Pointer of a contiguous tensor of exactly this type and shape (None passes)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    return _on_device(t, name).data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t.data_ptr()
 
 
-def _extent_strides(t: torch.Tensor) -> ctypes.Array:
-    """(batch, token, head) strides; the stride of a dimension of one entry is never used, so
-    whatever it is, 0 is passed."""
-    s = [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)][:-1]
-    return _I64x3(*([0] * (3 - len(s)) + s))
-
-
-def _out(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> torch.Tensor:
-    """The output tensor: a new one, or the caller's after the checks that an output needs."""
+def _out(t: Optional[torch.Tensor], like: torch.Tensor, like_lay: _Layout, name: str, dev: int):
+    """(output tensor, its layout): a new one, or the caller's after the checks it needs."""
     if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    _tensor(t, name, (like.dim(),))
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    if any(st == 0 and n > 1 for st, n in zip(t.stride(), t.shape)):
+        t = torch.empty_like(like)
+        return t, _tensor(t, name, dev)
+    lay = _tensor(t, name, dev, (like.dim(),))
+    if lay.shape != like_lay.shape:
+        raise ValueError(f"{name} must have shape {like_lay.shape}")
+    if lay.expanded:
         raise ValueError(f"{name} must not be an expanded tensor")
-    return t
+    return t, lay
 
 
-def _workspace(workspace, need: int, like: torch.Tensor):
+def _workspace(workspace, need: int, like: torch.Tensor, dev: int):
     """(tensor, pointer, bytes): the caller's buffer, or a new one of `need` bytes."""
     if workspace is None:
         if need == 0:
             return None, None, 0
         workspace = torch.empty((need + 3) // 4, dtype=torch.float32, device=like.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on_device(workspace, "workspace")
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the current CUDA device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm):
-    """The arguments that both directions of qk_norm_rope share, checked: (shape arguments,
-    norm and rotation arguments, whatever must stay alive until the call)."""
+def _qk_shape(qs, ks):
+    """(B, N, Hq, Hk, d), the rows' dimensions and whether the batch is packed."""
+    one = qs if qs is not None else ks
+    if qs is not None and ks is not None and (qs[:-2] != ks[:-2] or qs[-1] != ks[-1]):
+        raise ValueError(f"q {qs} and k {ks} must agree in all but the heads")
+    B = 1 if len(one) == 3 else one[0]
+    return ((B, one[-3], 0 if qs is None else qs[-2], 0 if ks is None else ks[-2], one[-1]), one[:-2], len(one) == 3)
+
+
+def _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev):
+    """The arguments that both directions of qk_norm_rope share, checked: shape arguments,
+    norm and rotation arguments, the layouts of q and k."""
     if q is None and k is None:
         raise ValueError("q or k is needed")
-    for t, name in ((q, "q"), (k, "k")):
-        if t is not None:
-            _tensor(t, name)
-    t = q if q is not None else k
-    if q is not None and k is not None and (q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]):
-        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} must agree in all but the heads")
-    rows = tuple(t.shape[:-2])
-    B, N, d = (1 if t.dim() == 3 else t.shape[0]), t.shape[-3], t.shape[-1]
-    lp = _small(lengths, "lengths", torch.int32, (B,))
-    if lengths is not None and t.dim() == 3:
-        raise ValueError("a packed batch has no lengths: all of its rows are valid")
-    wp = [_small(w, name, torch.float32, (d,)) for w, name in ((wq, "wq"), (wk, "wk"))]
-    rot, sec, ip, pp, sa, sb = 0, None, None, None, 0, 0
+    ql = None if q is None else _tensor(q, "q", dev)
+    kl = None if k is None else _tensor(k, "k", dev)
+    key = (ql, kl)
+    got = _qk_shapes.get(key)
+    if got is None:
+        got = _remember(_qk_shapes, key, _qk_shape(ql and ql.shape, kl and kl.shape))
+    head, rows, packed = got
+    lp = None
+    if lengths is not None:
+        if packed:
+            raise ValueError("a packed batch has no lengths: all of its rows are valid")
+        lp = _small(lengths, "lengths", torch.int32, head[:1], dev)
+    d = head[4:]
+    wqp, wkp = _small(wq, "wq", torch.float32, d, dev), _small(wk, "wk", torch.float32, d, dev)
+    rot = n_sec = sa = sb = 0
+    sec = ip = pp = None
     if inv_freq is not None:
         if positions is None:
             raise ValueError("a rotation needs positions")
-        if inv_freq.dim() != 1 or inv_freq.shape[0] < 1:
-            raise ValueError("inv_freq must be a tensor [rot_dim / 2]")
-        ip = _small(inv_freq, "inv_freq", torch.float64, inv_freq.shape)
-        rot = 2 * inv_freq.shape[0]
-        sec = [int(x) for x in sections] if sections is not None else [rot // 2]
-        if len(sec) < 1 or sum(sec) != rot // 2 or min(sec) < 0:
-            raise ValueError(f"sections must be counts that add up to {rot // 2}")
-        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
-            raise ValueError("positions must be an int32 tensor")
-        if len(sec) == 1 and tuple(positions.shape) == rows:
-            positions = positions[None]
-        if tuple(positions.shape) != (len(sec),) + rows:
-            raise ValueError(f"positions must have shape {(len(sec),) + rows}")
-        if positions.stride(-1) != 1 and positions.shape[-1] > 1:
+        pairs = inv_freq.numel()
+        ip = _small(inv_freq, "inv_freq", torch.float64, (pairs,), dev)
+        rot = 2 * pairs
+        key = None if sections is None else tuple(sections)
+        sec = _section_arrays.get((pairs, key))
+        if sec is None:
+            counts = [int(x) for x in key] if key is not None else [pairs]
+            if pairs < 1 or not counts or sum(counts) != pairs or min(counts) < 0:
+                raise ValueError(f"sections must be counts that add up to {pairs}")
+            sec = _remember(_section_arrays, (pairs, key), (_i32 * len(counts))(*counts))
+        n_sec = len(sec)
+        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or positions.get_device() != dev:
+            raise ValueError("positions must be an int32 tensor on the current CUDA device")
+        ps = positions.shape
+        st = positions.stride()
+        if n_sec == 1 and ps == rows:
+            st = (0,) + st
+        elif ps != (n_sec,) + rows:
+            raise ValueError(f"positions must have shape {(n_sec,) + rows}")
+        if st[-1] != 1 and ps[-1] > 1:
             raise ValueError("positions: the rows must be contiguous")
-        pp = _on_device(positions, "positions").data_ptr()
-        sa, sb = positions.stride(0), (positions.stride(1) if positions.dim() == 3 else 0)
+        pp = positions.data_ptr()
+        sa, sb = st[0], (0 if packed else st[1])
     elif positions is not None or sections is not None:
         raise ValueError("positions and sections need inv_freq")
-    n_sec = len(sec) if sec else 0
-    c_sec = (_i32 * n_sec)(*sec) if sec else None
-    heads = [0 if x is None else x.shape[-2] for x in (q, k)]
-    return ((B, N, heads[0], heads[1], d, lp),
-            (wp[0], wp[1], int(bool(norm)), float(eps), rot, int(bool(interleaved)), n_sec, c_sec, ip, pp, sa, sb),
-            (positions, c_sec))
+    return (*head, lp), (wqp, wkp, 1 if norm else 0, eps, rot, 1 if interleaved else 0, n_sec, sec, ip, pp, sa, sb), ql, kl
 
 
-def _pair(t):
-    return (None, _I64x3(0, 0, 0)) if t is None else (t.data_ptr(), _extent_strides(t))
+def _pair(t, lay):
+    return (None, _NO_STRIDES) if t is None else (t.data_ptr(), lay.strides)
 
 
 def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None, sections=None,
@@ -551,15 +597,17 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, 
     [B, N, H, d] or packed [T, H, d] (either may be None); wq, wk fp32 [d]; inv_freq fp64
     [pairs]; positions int32 [axes, B, N] resp. [axes, T] (one axis: that dimension may be
     left out); sections: pairs of each axis.  Pad rows (lengths int32 [B]) come out as 0."""
-    head, rot, alive = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm)
-    yq = None if q is None else _out(out_q, q, "out_q")
-    yk = None if k is None else _out(out_k, k, "out_k")
-    if head[0] * head[1] * (head[2] + head[3]) > 0:
-        _check(_lib.sigattn_qk_norm_rope(*head, *_pair(q), *_pair(k), *rot, *_pair(yq), *_pair(yk), _stream(stream)),
-               "qk_norm_rope")
+    dev = _here()
+    head, rot, ql, kl = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev)
+    yq, yql = (None, None) if q is None else _out(out_q, q, ql, "out_q", dev)
+    yk, ykl = (None, None) if k is None else _out(out_k, k, kl, "out_k", dev)
+    if head[0] and head[1] and head[2] + head[3]:
+        _check(_lib.sigattn_qk_norm_rope(*head, *_pair(q, ql), *_pair(k, kl), *rot, *_pair(yq, yql), *_pair(yk, ykl),
+                                         _stream(stream)), "qk_norm_rope")
     return yq, yk
 
 
+@functools.lru_cache(maxsize=_MEMO_ENTRIES)
 def qk_norm_rope_bwd_workspace_bytes(B: int, N: int, d: int) -> int:
     n = ctypes.c_size_t()
     _check(_lib.sigattn_qk_norm_rope_bwd_workspace_size(B, N, d, ctypes.byref(n)), "qk_norm_rope_bwd_workspace_size")
@@ -572,62 +620,72 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
     """(dq, dk, dwq, dwk) from the gradients dyq, dyk of qk_norm_rope's outputs; dwq, dwk are
     fp32 [d], None for a weight that is None.  ``workspace``: a contiguous CUDA buffer of
     qk_norm_rope_bwd_workspace_bytes bytes (allocated here if None and needed)."""
-    head, rot, alive = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm)
-    outs, grads = [], []
-    for x, dy, w, dx, name in ((q, dyq, wq, dq, "q"), (k, dyk, wk, dk, "k")):
+    dev = _here()
+    head, rot, ql, kl = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev)
+    args, outs, grads = [], [], []
+    for x, lay, dy, w, dx, name in ((q, ql, dyq, wq, dq, "q"), (k, kl, dyk, wk, dk, "k")):
         if x is None:
             if dy is not None or w is not None or dx is not None:
                 raise ValueError(f"gradients or weights of an absent {name}")
+            args.append((None, _NO_STRIDES, None, _NO_STRIDES))
             outs.append(None)
             grads.append(None)
             continue
-        if _tensor(dy, "dy" + name, (x.dim(),)).shape != x.shape:
-            raise ValueError(f"dy{name} must have shape {tuple(x.shape)}")
-        outs.append(_out(dx, x, "d" + name))
+        dyl = _tensor(dy, "dy" + name, dev)
+        if dyl.shape != lay.shape:
+            raise ValueError(f"dy{name} must have shape {lay.shape}")
+        dx, dxl = _out(dx, x, lay, "d" + name, dev)
+        args.append((dy.data_ptr(), dyl.strides, dx.data_ptr(), dxl.strides))
+        outs.append(dx)
         grads.append(None if w is None else torch.empty_like(w))
-    if head[0] * head[1] * (head[2] + head[3]) == 0:
+    gq, gk = grads
+    if not (head[0] and head[1] and head[2] + head[3]):
         return outs[0], outs[1], *(None if g is None else g.zero_() for g in grads)
-    need = qk_norm_rope_bwd_workspace_bytes(head[0], head[1], head[4]) if any(g is not None for g in grads) else 0
-    ws, wp, wn = _workspace(workspace, need, outs[0] if outs[0] is not None else outs[1])
-    ptr = lambda g: None if g is None else g.data_ptr()
-    _check(_lib.sigattn_qk_norm_rope_bwd(*head, *_pair(q), *_pair(k), *_pair(dyq), *_pair(dyk), *rot,
-                                         *_pair(outs[0]), *_pair(outs[1]), ptr(grads[0]), ptr(grads[1]), wp, wn,
-                                         _stream(stream)), "qk_norm_rope_bwd")
-    return outs[0], outs[1], grads[0], grads[1]
+    need = qk_norm_rope_bwd_workspace_bytes(head[0], head[1], head[4]) if gq is not None or gk is not None else 0
+    ws, wp, wn = _workspace(workspace, need, q if q is not None else k, dev)
+    _check(_lib.sigattn_qk_norm_rope_bwd(*head, *_pair(q, ql), *_pair(k, kl), *args[0][:2], *args[1][:2], *rot,
+                                         *args[0][2:], *args[1][2:], None if gq is None else gq.data_ptr(),
+                                         None if gk is None else gk.data_ptr(), wp, wn, _stream(stream)),
+           "qk_norm_rope_bwd")
+    return outs[0], outs[1], gq, gk
 
 
+@functools.lru_cache(maxsize=_MEMO_ENTRIES)
 def linear_workspace_bytes(B: int, N: int, H: int, d: int, backward: bool = False) -> int:
     n = ctypes.c_size_t()
-    _check(_lib.sigattn_linear_workspace_size(B, N, H, d, int(bool(backward)), ctypes.byref(n)), "linear_workspace_size")
+    _check(_lib.sigattn_linear_workspace_size(B, N, H, d, 1 if backward else 0, ctypes.byref(n)), "linear_workspace_size")
     return n.value
 
 
-def _linear_args(tensors, log_decay, lengths, cu_seqlens, max_seqlen, states):
-    """The shape arguments that linear_fwd and linear_bwd share, checked."""
-    q = tensors[0][0]
-    for t, name in tensors:
-        _tensor(t, name, (q.dim(),) if isinstance(q, torch.Tensor) and q.dim() in (3, 4) else (3, 4))
-        if t.shape != q.shape:
-            raise ValueError(f"{name} must have q's shape {tuple(q.shape)}")
-    H, d = q.shape[-2:]
+def _linear_args(q, others, log_decay, lengths, cu_seqlens, max_seqlen, states, dev):
+    """The arguments that linear_fwd and linear_bwd share, checked: shape arguments, pointers
+    of the states, and pointer and strides of q and the others."""
+    lay = _tensor(q, "q", dev)
+    pairs = [q.data_ptr(), lay.strides]
+    for t, name in others:
+        x = _tensor(t, name, dev)
+        if x is not lay and x.shape != lay.shape:
+            raise ValueError(f"{name} must have q's shape {lay.shape}")
+        pairs += (t.data_ptr(), x.strides)
+    *rows, H, d = lay.shape
     lp = cp = None
-    if q.dim() == 3:
+    if len(rows) == 1:
         if cu_seqlens is None or max_seqlen is None or lengths is not None:
             raise ValueError("a packed batch takes cu_seqlens and max_seqlen, no lengths")
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor [B + 1]")
-        cp = _small(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape)
-        B, N, T = cu_seqlens.shape[0] - 1, int(max_seqlen), q.shape[0]
+        cp = _small(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+        B, N, T = cu_seqlens.numel() - 1, int(max_seqlen), rows[0]
     else:
         if cu_seqlens is not None or max_seqlen is not None:
             raise ValueError("a padded batch takes lengths, no cu_seqlens or max_seqlen")
-        B, N, T = q.shape[0], q.shape[1], 0
-        lp = _small(lengths, "lengths", torch.int32, (B,))
-    gp = _small(log_decay, "log_decay", torch.float32, (H,))
+        (B, N), T = rows, 0
+        lp = _small(lengths, "lengths", torch.int32, (B,), dev)
+    gp = _small(log_decay, "log_decay", torch.float32, (H,), dev)
     if gp is None:
         raise ValueError("log_decay is needed")
-    ptrs = [_small(s, name, torch.float32, (B, H, d, d)) for s, name in states]
-    return (B, N, T, H, d, lp, cp, gp), ptrs
+    ptrs = [_small(s, name, torch.float32, (B, H, d, d), dev) for s, name in states]
+    return (B, N, T, H, d, lp, cp, gp), ptrs, pairs, lay
 
 
 def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None,
@@ -638,18 +696,19 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
     packed [T, H, d] (with cu_seqlens and max_seqlen); state fp32 [B, H, d, d] is what the
     sequences start from (None: 0).  The final state is returned where return_state is set or
     a buffer for it is given, else None."""
-    head, (sp, fp) = _linear_args(((q, "q"), (k, "k"), (v, "v")), log_decay, lengths, cu_seqlens, max_seqlen,
-                                  ((state, "state"), (final_state, "final_state")))
+    dev = _here()
+    head, (sp, fp), pairs, lay = _linear_args(q, ((k, "k"), (v, "v")), log_decay, lengths, cu_seqlens, max_seqlen,
+                                              ((state, "state"), (final_state, "final_state")), dev)
     B, N, _, H, d = head[:5]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out = _out(out, q, "out")
+    out, ol = _out(out, q, lay, "out", dev)
     if return_state and final_state is None:
         final_state = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
         fp = final_state.data_ptr()
-    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q)
-    _check(_lib.sigattn_linear_fwd(*head, float(scale), *_pair(q), *_pair(k), *_pair(v), sp, *_pair(out), fp, wp, wn,
-                                   _stream(stream)), "linear_fwd")
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev)
+    _check(_lib.sigattn_linear_fwd(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, wp, wn, _stream(stream)),
+           "linear_fwd")
     return out, final_state
 
 
@@ -658,18 +717,20 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
     """(dq, dk, dv, dstate_out): gradients of linear_fwd from do and, for a loss that uses the
     final state, its gradient ``dstate``.  dstate_out, the gradient of ``state``, is None where
     there was no state (unless a buffer for it is given)."""
-    head, (sp, ep, gp) = _linear_args(((q, "q"), (k, "k"), (v, "v"), (do, "do")), log_decay, lengths, cu_seqlens,
-                                      max_seqlen, ((state, "state"), (dstate, "dstate"), (dstate_out, "dstate_out")))
+    dev = _here()
+    head, (sp, ep, gp), pairs, lay = _linear_args(
+        q, ((k, "k"), (v, "v"), (do, "do")), log_decay, lengths, cu_seqlens, max_seqlen,
+        ((state, "state"), (dstate, "dstate"), (dstate_out, "dstate_out")), dev)
     B, N, _, H, d = head[:5]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq, dk, dv = _out(dq, q, "dq"), _out(dk, k, "dk"), _out(dv, v, "dv")
+    (dq, dql), (dk, dkl), (dv, dvl) = _out(dq, q, lay, "dq", dev), _out(dk, k, lay, "dk", dev), _out(dv, v, lay, "dv", dev)
     if state is not None and dstate_out is None:
         dstate_out = torch.empty_like(state)
         gp = dstate_out.data_ptr()
-    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q)
-    _check(_lib.sigattn_linear_bwd(*head, float(scale), *_pair(q), *_pair(k), *_pair(v), *_pair(do), sp, ep,
-                                   *_pair(dq), *_pair(dk), *_pair(dv), gp, wp, wn, _stream(stream)), "linear_bwd")
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev)
+    _check(_lib.sigattn_linear_bwd(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,
+                                   dv.data_ptr(), dvl.strides, gp, wp, wn, _stream(stream)), "linear_bwd")
     return dq, dk, dv, dstate_out
 
 
@@ -678,23 +739,24 @@ def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] 
     """o of one token of each sequence, q, k, v bf16 [B, H, d]; ``state`` fp32 [B, H, d, d] is
     updated in place, or kept and its update written to ``state_out``.  Sequences with
     lengths[b] = 0 have no token: o is 0 and their state stays."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _tensor(t, name, (3,))
-        if t.shape != q.shape:
-            raise ValueError(f"{name} must have q's shape {tuple(q.shape)}")
-    B, H, d = q.shape
-    lp = _small(lengths, "lengths", torch.int32, (B,))
-    gp = _small(log_decay, "log_decay", torch.float32, (H,))
-    sp = _small(state, "state", torch.float32, (B, H, d, d))
+    dev = _here()
+    ql, kl, vl = _tensor(q, "q", dev, (3,)), _tensor(k, "k", dev, (3,)), _tensor(v, "v", dev, (3,))
+    if kl.shape != ql.shape or vl.shape != ql.shape:
+        raise ValueError(f"k and v must have q's shape {ql.shape}")
+    B, H, d = ql.shape
+    square = (B, H, d, d)
+    lp = _small(lengths, "lengths", torch.int32, (B,), dev)
+    gp = _small(log_decay, "log_decay", torch.float32, (H,), dev)
+    sp = _small(state, "state", torch.float32, square, dev)
     if gp is None or sp is None:
         raise ValueError("log_decay and state are needed")
-    np_ = sp if state_out is None else _small(state_out, "state_out", torch.float32, (B, H, d, d))
+    np_ = sp if state_out is None else _small(state_out, "state_out", torch.float32, square, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out = _out(out, q, "out")
-    two = lambda t: (t.data_ptr(), _I64x2(*[st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)][:2]))
-    _check(_lib.sigattn_linear_step(B, H, d, lp, gp, float(scale), *two(q), *two(k), *two(v), sp, np_, *two(out),
-                                    _stream(stream)), "linear_step")
+    out, ol = _out(out, q, ql, "out", dev)
+    _check(_lib.sigattn_linear_step(B, H, d, lp, gp, scale, q.data_ptr(), ql.strides2, k.data_ptr(), kl.strides2,
+                                    v.data_ptr(), vl.strides2, sp, np_, out.data_ptr(), ol.strides2, _stream(stream)),
+           "linear_step")
     return out
 
 

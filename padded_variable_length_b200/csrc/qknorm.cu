@@ -11,8 +11,14 @@
 // Layout of the work: d / 16 lanes share a row and each lane holds the two 8-value pieces
 // whose pairs it turns (halves: pieces c and c + rot_dim/16; side by side: any two), so that
 // the rotation needs no exchange between lanes and the norm two or three shuffles.  A warp
-// takes one token at a time and walks its heads, 512 / d of them per step; the angles'
-// sines and cosines are computed once per token and serve every head.
+// takes one token of q or of k at a time and walks its heads, 512 / d of them per step.  The
+// lanes of a step's rows compute the sines and cosines of a token together, one or two pairs
+// each, and exchange them: they serve every head.
+//
+// What bounds it is the memory, 4 bytes an element forward and 6 backward, if enough loads
+// are in flight: each lane keeps the pieces of its next kDepth steps on their way into shared
+// memory slots of its own (cp.async; nobody else reads them, so a step waits for its own
+// copies alone).
 //
 // Angles: with inv_freq / 2 pi kept as a 64-bit fraction F of a turn, position * F modulo
 // 2^64 is the angle modulo one turn with no rounding that grows with the position, so far
@@ -31,7 +37,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxAxes = 4;
-constexpr int kMaxBlocks = 148 * 8;  // also the rows of the backward's partial weight sums
+// a warp's token index steps past the last one by at most the grid's warps (148 * 3 * 8)
+constexpr int64_t kMaxTokens = 0x7FFFFFFF - 16384;
+constexpr int kDepth = 4;         // steps whose loads are in flight
+constexpr int kSms = 148;         // B200
+constexpr int kPerSm[2] = {3, 2};  // resident blocks, forward and backward
 
 struct QkTensor {
   const uint4* x;
@@ -54,7 +64,8 @@ struct QkParams {
   const double* inv_freq;
   const int32_t* pos;
   int64_t pos_sa, pos_sb;
-  float* partial;  // backward: [gridDim.x][2][d] sums of g u, nullptr without weights
+  int blocks0;     // blocks [0, blocks0) take the queries, the others the keys
+  float* partial;  // backward: [gridDim.x][d] sums of g u, nullptr without weights
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, float* f) {
@@ -77,86 +88,69 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // What a lane knows of its place in a row: its two pieces and the pairs that they form.
 template <int D>
 struct Lane {
-  static constexpr int kLanes = D / 16;     // lanes of a row
+  static constexpr int kLanes = D / 16;      // lanes of a row
   static constexpr int kRows = 32 / kLanes;  // rows of a warp's step
-  int c0, c1;       // pieces
-  int sub;          // row of the step
-  bool turns[2];    // halves: both the same; side by side: of each piece
-  uint64_t frac[8];  // turns per position of the lane's pairs, in 2^-64
-  uint32_t axis;    // their axes, 4 bits each
+  static constexpr int kOwn = 8 / kRows;     // pairs of the lane's eight that it computes
+  int c0, c1;           // pieces
+  int sub;              // row of the step
+  uint64_t frac[kOwn];  // turns per position of the pairs it computes, in 2^-64
+  int axis[kOwn];       // their axes
 
   __device__ Lane(const QkParams& p) {
     const int l = threadIdx.x % 32 % kLanes;
     sub = threadIdx.x % 32 / kLanes;
-    int pair[8];
-    if (p.interleaved) {
-      c0 = l;
-      c1 = l + kLanes;
-      turns[0] = c0 * 8 < p.rot_dim;
-      turns[1] = c1 * 8 < p.rot_dim;
+    const int r = p.rot_dim / 16;  // turned pieces of a half
+    c0 = p.interleaved || l < r ? l : 2 * l;  // halves: behind 2 r pieces the rest pair up
+    c1 = p.interleaved ? l + kLanes : l < r ? l + r : 2 * l + 1;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pair[i] = i < 4 ? 4 * c0 + i : 4 * c1 + i - 4;
-    } else {
-      const int r = p.rot_dim / 16;
-      turns[0] = turns[1] = l < r;
-      c0 = l < r ? l : 2 * l;  // behind the 2r turned pieces the rest pair up in order
-      c1 = l < r ? l + r : 2 * l + 1;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) pair[i] = 8 * l + i;
-    }
-    axis = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      frac[i] = 0;
-      if (turns[i / 4]) {
+    for (int x = 0; x < kOwn; ++x) {
+      const int i = sub * kOwn + x;  // of the lane's eight pairs
+      const int pair = !p.interleaved ? 8 * l + i : i < 4 ? 4 * c0 + i : 4 * c1 + i - 4;
+      frac[x] = 0;
+      axis[x] = 0;
+      if (p.interleaved ? 2 * pair < p.rot_dim : l < r) {
         // inv_freq / 2 pi without its whole turns; scaling by 2^64 is exact
-        double f = p.inv_freq[pair[i]] * 0.15915494309189533577;
+        double f = p.inv_freq[pair] * 0.15915494309189533577;
         f -= floor(f);
-        frac[i] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0;
-        uint32_t a = 0;
-        while (a + 1 < static_cast<uint32_t>(p.axes) && pair[i] >= p.axis_end[a]) ++a;
-        axis |= a << (4 * i);
+        frac[x] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0;
+        while (axis[x] + 1 < p.axes && pair >= p.axis_end[axis[x]]) ++axis[x];
       }
     }
   }
 
-  // cos and sin of the lane's eight angles at token (b, i)
-  __device__ void angles(const QkParams& p, int b, int i, float* cs, float* sn) const {
-    if (p.rot_dim == 0) {
+  // cos and sin of the lane's eight angles at the positions pos[axis]
+  __device__ __forceinline__ void angles(const int32_t* pos, float* cs, float* sn) const {
+    float c[kOwn], s[kOwn];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
-      return;
+    for (int x = 0; x < kOwn; ++x) {
+      const uint64_t turn = frac[x] * static_cast<uint64_t>(static_cast<int64_t>(pos[axis[x]]));
+      // the high word as a signed fraction of half turns in [-1, 1)
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[x], &c[x]);
     }
-    const int32_t* at = p.pos + b * p.pos_sb + i;
-    int32_t x[kMaxAxes];
-#pragma unroll
-    for (int a = 0; a < kMaxAxes; ++a) x[a] = a < p.axes ? at[a * p.pos_sa] : 0;
+    const int l = threadIdx.x % 32 % kLanes;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t a = (axis >> (4 * j)) & 15u;
-      const int32_t pos = a == 0 ? x[0] : a == 1 ? x[1] : a == 2 ? x[2] : x[3];
-      const uint64_t turn = frac[j] * static_cast<uint64_t>(static_cast<int64_t>(pos));
-      // the high word as a signed fraction of half turns in [-1, 1)
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[j], &cs[j]);
+      cs[j] = __shfl_sync(0xFFFFFFFFu, c[j % kOwn], j / kOwn * kLanes + l);
+      sn[j] = __shfl_sync(0xFFFFFFFFu, s[j % kOwn], j / kOwn * kLanes + l);
     }
   }
 
-  // y = R z (way = 1) or R^T z (way = -1) on the lane's two pieces z[0..7], z[8..15]
-  __device__ __forceinline__ static void turn(bool interleaved, float way, const float* cs,
-                                              const float* sn, float* z) {
+  // y = R z, or R^T z with the sines negated, on the lane's two pieces z[0..7], z[8..15]
+  __device__ __forceinline__ static void turn(bool interleaved, const float* cs, const float* sn,
+                                              float* z) {
     if (interleaved) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float a = z[2 * j], b = z[2 * j + 1], s = way * sn[j];
-        z[2 * j] = a * cs[j] - b * s;
-        z[2 * j + 1] = a * s + b * cs[j];
+        const float a = z[2 * j], b = z[2 * j + 1];
+        z[2 * j] = a * cs[j] - b * sn[j];
+        z[2 * j + 1] = a * sn[j] + b * cs[j];
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float a = z[j], b = z[j + 8], s = way * sn[j];
-        z[j] = a * cs[j] - b * s;
-        z[j + 8] = a * s + b * cs[j];
+        const float a = z[j], b = z[j + 8];
+        z[j] = a * cs[j] - b * sn[j];
+        z[j + 8] = a * sn[j] + b * cs[j];
       }
     }
   }
@@ -169,176 +163,225 @@ struct Lane {
   }
 };
 
-__device__ __forceinline__ void load_weights(const float* w, int c0, int c1, float* f) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = w ? __ldg(w + (i < 8 ? c0 : c1) * 8 + (i & 7)) : 1.0f;
+__device__ __forceinline__ void copy16(void* dst, const uint4* src, bool have) {
+  // without a source 16 zero bytes are written
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(have ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const int32_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) k_qk_fwd(const QkParams p) {
-  using L = Lane<D>;
-  const L lane(p);
-  float w[2][16];
-  load_weights(p.t[0].w, lane.c0, lane.c1, w[0]);
-  load_weights(p.t[1].w, lane.c0, lane.c1, w[1]);
-  const int step = gridDim.x * kWarps;
-  for (int tok = blockIdx.x * kWarps + threadIdx.x / 32; tok < p.tokens; tok += step) {
-    const int b = tok / p.N, i = tok % p.N;
-    const bool valid = !p.lengths || i < __ldg(p.lengths + b);
-    float cs[8], sn[8];
-    if (valid) lane.angles(p, b, i, cs, sn);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const QkTensor& t = p.t[m];
-      const uint4* x = t.x + b * t.x_sb + i * t.x_sn;
-      uint4* y = t.y + b * t.y_sb + i * t.y_sn;
-      for (int h0 = 0; h0 < t.H; h0 += L::kRows) {
-        const int h = h0 + lane.sub;
-        const bool have = h < t.H;
-        if (!valid) {
-          if (have) {
-            y[h * t.y_sh + lane.c0] = make_uint4(0u, 0u, 0u, 0u);
-            y[h * t.y_sh + lane.c1] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          continue;
-        }
-        uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
-        if (have) {
-          r0 = x[h * t.x_sh + lane.c0];
-          r1 = x[h * t.x_sh + lane.c1];
-        }
-        float z[16];
-        unpack8(r0, z);
-        unpack8(r1, z + 8);
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s = fmaf(z[j], z[j], s);
-        s = L::row_sum(s);
-        const float r = p.norm ? rsqrtf(fmaf(s, p.inv_d, p.eps)) : 1.0f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] *= r * w[m][j];
-        L::turn(p.interleaved, 1.0f, cs, sn, z);
-        if (have) {
-          y[h * t.y_sh + lane.c0] = pack8(z);
-          y[h * t.y_sh + lane.c1] = pack8(z + 8);
-        }
-      }
+// One step of a warp: its slot in shared memory.  piece[x][lane]: the lane's two pieces of x,
+// and of dy in the backward.
+template <int PIECES>
+struct Slot {
+  uint4 piece[PIECES][32];
+  int32_t pos[kMaxAxes];
+};
+
+// A warp's walk over the steps of its tokens.
+struct Walk {
+  int tok, h, b, i;  // token, first head of the step, batch entry and row
+  bool valid;
+  __device__ __forceinline__ void enter(const QkParams& p) {
+    b = tok / p.N;
+    i = tok - b * p.N;
+    valid = tok < p.tokens && (!p.lengths || i < __ldg(p.lengths + b));
+  }
+  __device__ __forceinline__ void next(const QkParams& p, int H, int rows, int stride) {
+    h += rows;
+    if (h >= H) {
+      h = 0;
+      tok += stride;
+      if (tok < p.tokens) enter(p);
     }
   }
-}
+};
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) k_qk_bwd(const QkParams p) {
+// Forward (GRAD false) and backward.  In the backward y takes the gradient of x.
+template <int D, bool GRAD>
+__global__ void __launch_bounds__(kThreads, kPerSm[GRAD]) k_qk(const QkParams p) {
   using L = Lane<D>;
+  constexpr int kPieces = GRAD ? 4 : 2;
+  extern __shared__ uint4 smem[];
+  const int warp = threadIdx.x / 32, ln = threadIdx.x % 32;
+  Slot<kPieces>* slots = reinterpret_cast<Slot<kPieces>*>(smem) + warp * kDepth;
+  const bool keys = static_cast<int>(blockIdx.x) >= p.blocks0;
+  const QkTensor& t = p.t[keys];
+  const int block = keys ? blockIdx.x - p.blocks0 : blockIdx.x;
+  const int stride = (keys ? gridDim.x - p.blocks0 : p.blocks0) * kWarps;
   const L lane(p);
-  float w[2][16], dw[2][16];
-  load_weights(p.t[0].w, lane.c0, lane.c1, w[0]);
-  load_weights(p.t[1].w, lane.c0, lane.c1, w[1]);
-#pragma unroll
-  for (int j = 0; j < 16; ++j) dw[0][j] = dw[1][j] = 0.0f;
-  const int step = gridDim.x * kWarps;
-  for (int tok = blockIdx.x * kWarps + threadIdx.x / 32; tok < p.tokens; tok += step) {
-    const int b = tok / p.N, i = tok % p.N;
-    const bool valid = !p.lengths || i < __ldg(p.lengths + b);
-    float cs[8], sn[8];
-    if (valid) lane.angles(p, b, i, cs, sn);
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const QkTensor& t = p.t[m];
-      const uint4* x = t.x + b * t.x_sb + i * t.x_sn;
-      const uint4* dy = t.dy + b * t.dy_sb + i * t.dy_sn;
-      uint4* dx = t.y + b * t.y_sb + i * t.y_sn;
-      for (int h0 = 0; h0 < t.H; h0 += L::kRows) {
-        const int h = h0 + lane.sub;
+
+  Walk ahead{block * kWarps + warp, 0, 0, 0, false};
+  ahead.enter(p);
+  Walk at = ahead;
+  auto fetch = [&](Slot<kPieces>& s) {
+    if (ahead.tok < p.tokens) {
+      if (ahead.valid) {
+        const int h = ahead.h + lane.sub;
         const bool have = h < t.H;
-        if (!valid) {
-          if (have) {
-            dx[h * t.y_sh + lane.c0] = make_uint4(0u, 0u, 0u, 0u);
-            dx[h * t.y_sh + lane.c1] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          continue;
+        const uint4* x = t.x + ahead.b * t.x_sb + ahead.i * t.x_sn + (have ? h : 0) * t.x_sh;
+        copy16(&s.piece[0][ln], x + lane.c0, have);
+        copy16(&s.piece[1][ln], x + lane.c1, have);
+        if constexpr (GRAD) {
+          const uint4* g = t.dy + ahead.b * t.dy_sb + ahead.i * t.dy_sn + (have ? h : 0) * t.dy_sh;
+          copy16(&s.piece[2][ln], g + lane.c0, have);
+          copy16(&s.piece[3][ln], g + lane.c1, have);
         }
-        uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0, g0 = r0, g1 = r0;
-        if (have) {
-          r0 = x[h * t.x_sh + lane.c0];
-          r1 = x[h * t.x_sh + lane.c1];
-          g0 = dy[h * t.dy_sh + lane.c0];
-          g1 = dy[h * t.dy_sh + lane.c1];
-        }
-        float u[16], g[16];
-        unpack8(r0, u);
-        unpack8(r1, u + 8);
-        unpack8(g0, g);
-        unpack8(g1, g + 8);
-        L::turn(p.interleaved, -1.0f, cs, sn, g);
-        float s = 0.0f;
+        if (ahead.h == 0 && ln < p.axes)
+          copy4(&s.pos[ln], p.pos + ln * p.pos_sa + ahead.b * p.pos_sb + ahead.i);
+      }
+      ahead.next(p, t.H, L::kRows, stride);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s = fmaf(u[j], u[j], s);
-        s = L::row_sum(s);
+  for (int s = 0; s < kDepth - 1; ++s) fetch(slots[s]);
+
+  float w[16], dw[16], cs[8], sn[8];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    w[j] = t.w ? __ldg(t.w + (j < 8 ? lane.c0 : lane.c1) * 8 + (j & 7)) : 1.0f;
+    dw[j] = 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
+
+  for (int n = 0; at.tok < p.tokens; ++n) {
+    Slot<kPieces>& s = slots[n % kDepth];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+    const int h = at.h + lane.sub;
+    const bool have = h < t.H;
+    uint4* y = t.y + at.b * t.y_sb + at.i * t.y_sn + (have ? h : 0) * t.y_sh;
+    if (at.valid) {
+      if (at.h == 0 && p.rot_dim > 0) {
+        __syncwarp();  // the positions were copied by other lanes
+        lane.angles(s.pos, cs, sn);
+        if (GRAD)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
+      }
+      float z[16], g[16];
+      unpack8(s.piece[0][ln], z);
+      unpack8(s.piece[1][ln], z + 8);
+      if constexpr (GRAD) {
+        unpack8(s.piece[2][ln], g);
+        unpack8(s.piece[3][ln], g + 8);
+        L::turn(p.interleaved, cs, sn, g);
+      }
+      float r = 1.0f;
+      if (p.norm) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum = fmaf(z[j], z[j], sum);
+        r = rsqrtf(fmaf(L::row_sum(sum), p.inv_d, p.eps));
+      }
+      if constexpr (!GRAD) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) z[j] *= r * w[j];
+        L::turn(p.interleaved, cs, sn, z);
+        if (have) {
+          y[lane.c0] = pack8(z);
+          y[lane.c1] = pack8(z + 8);
+        }
+      } else {
         // a lane without a row has u = g = 0 and, with r = 0 (not rsqrt(eps)), adds nothing
-        const float r = !have ? 0.0f : p.norm ? rsqrtf(fmaf(s, p.inv_d, p.eps)) : 1.0f;
+        if (!have) r = 0.0f;
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          u[j] *= r;
-          dw[m][j] = fmaf(g[j], u[j], dw[m][j]);
-          g[j] *= w[m][j];
-          dot = fmaf(g[j], u[j], dot);
+          z[j] *= r;
+          dw[j] = fmaf(g[j], z[j], dw[j]);
+          g[j] *= w[j];
+          dot = fmaf(g[j], z[j], dot);
         }
         dot = p.norm ? L::row_sum(dot) * p.inv_d : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) g[j] = r * fmaf(-u[j], dot, g[j]);
+        for (int j = 0; j < 16; ++j) g[j] = r * fmaf(-z[j], dot, g[j]);
         if (have) {
-          dx[h * t.y_sh + lane.c0] = pack8(g);
-          dx[h * t.y_sh + lane.c1] = pack8(g + 8);
+          y[lane.c0] = pack8(g);
+          y[lane.c1] = pack8(g + 8);
         }
       }
+    } else if (have) {
+      y[lane.c0] = make_uint4(0u, 0u, 0u, 0u);
+      y[lane.c1] = make_uint4(0u, 0u, 0u, 0u);
     }
+    at.next(p, t.H, L::kRows, stride);
+    __syncwarp();  // every lane has read the positions of the slot that is filled next
+    fetch(slots[(n + kDepth - 1) % kDepth]);
   }
-  if (!p.partial) return;
+  if (!GRAD || !p.partial) return;
   // The block's sums, in a fixed order: the rows of each warp by shuffles, the warps one
   // after another from shared memory.
-  __shared__ float sums[kWarps][2][D];
+  __shared__ float sums[kWarps][D];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int j = 0; j < 16; ++j) {
+    float v = dw[j];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float v = dw[m][j];
-#pragma unroll
-      for (int o = 16; o >= L::kLanes; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      if (lane.sub == 0) sums[threadIdx.x / 32][m][(j < 8 ? lane.c0 : lane.c1) * 8 + (j & 7)] = v;
-    }
+    for (int o = 16; o >= L::kLanes; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (lane.sub == 0) sums[warp][(j < 8 ? lane.c0 : lane.c1) * 8 + (j & 7)] = v;
+  }
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+  if (threadIdx.x < D) {
     float v = 0.0f;
 #pragma unroll
-    for (int x = 0; x < kWarps; ++x) v += sums[x][c / D][c % D];
-    p.partial[static_cast<int64_t>(blockIdx.x) * 2 * D + c] = v;
+    for (int x = 0; x < kWarps; ++x) v += sums[x][threadIdx.x];
+    p.partial[blockIdx.x * D + threadIdx.x] = v;
   }
 }
 
-// dwq, dwk from the blocks' partial sums [rows][2 d]: one block per 32 columns, its warps
-// take the rows in turn (coalesced 128-byte reads) and are added in a fixed order.
-__global__ void __launch_bounds__(1024) k_qk_dw(const float* __restrict__ partial, int rows,
-                                                int d, float* __restrict__ dwq,
+// dwq, dwk from the blocks' partial sums [rows][d], the first rows0 of them of the queries:
+// one block per 32 columns of one of the two, its warps take the rows in turn (coalesced
+// 128-byte reads) and are added in a fixed order.
+__global__ void __launch_bounds__(1024) k_qk_dw(const float* __restrict__ partial, int rows0,
+                                                int rows, int d, float* __restrict__ dwq,
                                                 float* __restrict__ dwk) {
   __shared__ float sums[32][33];
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const bool keys = static_cast<int>(blockIdx.x) >= d / 32;
+  const int c0 = (blockIdx.x % (d / 32)) * 32;
+  float* out = keys ? dwk : dwq;
+  if (!out) return;
   float v = 0.0f;
-  for (int r = warp; r < rows; r += 32) v += partial[static_cast<int64_t>(r) * 2 * d + c];
+  for (int r = (keys ? rows0 : 0) + warp; r < (keys ? rows : rows0); r += 32)
+    v += partial[r * d + c0 + lane];
   sums[warp][lane] = v;
   __syncthreads();
   v = sums[lane][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  if (lane == 0) {
-    const int col = blockIdx.x * 32 + warp;
-    float* out = col < d ? dwq : dwk;
-    if (out) out[col % d] = v;
-  }
+  if (lane == 0) out[c0 + warp] = v;
 }
 
-int blocks_for(int tokens) { return std::min((tokens + kWarps - 1) / kWarps, kMaxBlocks); }
+// Blocks of the queries and of the keys: a warp per token of each, or as many as the GPU
+// holds at once, shared out by their heads.
+void blocks_for(int tokens, int Hq, int Hk, int most, int* q, int* k) {
+  const int need = (tokens + kWarps - 1) / kWarps;
+  const int64_t heads = static_cast<int64_t>(Hq) + Hk;
+  *q = Hq == 0 ? 0 : std::max<int>(1, std::min<int64_t>(need, static_cast<int64_t>(most) * Hq / heads));
+  *k = Hk == 0 ? 0 : std::max<int>(1, std::min<int64_t>(need, static_cast<int64_t>(most) * Hk / heads));
+}
+
+template <int D, bool GRAD>
+int launch_qk(QkParams& p, cudaStream_t stream) {
+  constexpr int bytes = kWarps * kDepth * sizeof(Slot<GRAD ? 4 : 2>);
+  int q, k;
+  blocks_for(p.tokens, p.t[0].H, p.t[1].H, kSms * kPerSm[GRAD], &q, &k);
+  p.blocks0 = q;
+  const auto kern = k_qk<D, GRAD>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_status(e);
+  kern<<<q + k, kThreads, bytes, stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
 
 int check_strided(const void* ptr, const int64_t* strides, int64_t s[3]) {
   if (!ptr || !strides) return SIGATTN_ERR_INVALID;
@@ -363,7 +406,7 @@ int check_common(int B, int N, int Hq, int Hk, int d, const int32_t* lengths, fl
   if (norm && !(std::isfinite(eps) && eps >= 0.0f)) return SIGATTN_ERR_INVALID;
   if (rot_dim < 0 || (interleaved != 0 && interleaved != 1)) return SIGATTN_ERR_INVALID;
   if (d != 64 && d != 128) return SIGATTN_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(B) * N > 0x7FFFFFFF - kMaxBlocks * kWarps) return SIGATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(B) * N > kMaxTokens) return SIGATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(Hq) + Hk > 0x3FFFFFFF) return SIGATTN_ERR_UNSUPPORTED;
   if (rot_dim > d || rot_dim % 16 != 0) return SIGATTN_ERR_UNSUPPORTED;
   *p = QkParams{};
@@ -442,16 +485,18 @@ extern "C" int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const i
   if ((rc = check_one(Hk, k, k_strides, nullptr, nullptr, false, yk, yk_strides, wk, &p.t[1])) !=
       SIGATTN_OK)
     return rc;
-  const auto kern = d == 64 ? k_qk_fwd<64> : k_qk_fwd<128>;
-  kern<<<blocks_for(p.tokens), kThreads, 0, static_cast<cudaStream_t>(s)>>>(p);
-  return cuda_status(cudaGetLastError());
+  const cudaStream_t stream = static_cast<cudaStream_t>(s);
+  return d == 64 ? launch_qk<64, false>(p, stream) : launch_qk<128, false>(p, stream);
 }
 
 extern "C" int sigattn_qk_norm_rope_bwd_workspace_size(int B, int N, int d, size_t* bytes) {
   if (!bytes || B < 1 || N < 1) return SIGATTN_ERR_INVALID;
-  if ((d != 64 && d != 128) || static_cast<int64_t>(B) * N > 0x7FFFFFFF - kMaxBlocks * kWarps)
+  if ((d != 64 && d != 128) || static_cast<int64_t>(B) * N > kMaxTokens)
     return SIGATTN_ERR_UNSUPPORTED;
-  *bytes = sizeof(float) * 2 * d * blocks_for(B * N);
+  // of any head counts: the queries' and the keys' blocks, one more where a share rounds up
+  const size_t most = std::min<size_t>(2 * ((static_cast<size_t>(B) * N + kWarps - 1) / kWarps),
+                                       kSms * kPerSm[1] + 1);
+  *bytes = sizeof(float) * d * most;
   return SIGATTN_OK;
 }
 
@@ -475,18 +520,18 @@ extern "C" int sigattn_qk_norm_rope_bwd(
   if ((rc = check_one(Hk, k, k_strides, dyk, dyk_strides, true, dk, dk_strides, wk, &p.t[1])) !=
       SIGATTN_OK)
     return rc;
-  const int blocks = blocks_for(p.tokens);
   if (dwq || dwk) {
-    if (!workspace || workspace_bytes < sizeof(float) * 2 * d * static_cast<size_t>(blocks))
-      return SIGATTN_ERR_INVALID;
+    size_t need = 0;
+    if ((rc = sigattn_qk_norm_rope_bwd_workspace_size(B, N, d, &need)) != SIGATTN_OK) return rc;
+    if (!workspace || workspace_bytes < need) return SIGATTN_ERR_INVALID;
     if (reinterpret_cast<uintptr_t>(workspace) & 15u) return SIGATTN_ERR_ALIGNMENT;
     p.partial = static_cast<float*>(workspace);
   }
   const cudaStream_t stream = static_cast<cudaStream_t>(s);
-  const auto kern = d == 64 ? k_qk_bwd<64> : k_qk_bwd<128>;
-  kern<<<blocks, kThreads, 0, stream>>>(p);
-  rc = cuda_status(cudaGetLastError());
+  rc = d == 64 ? launch_qk<64, true>(p, stream) : launch_qk<128, true>(p, stream);
   if (rc != SIGATTN_OK || !p.partial) return rc;
-  k_qk_dw<<<2 * d / 32, 1024, 0, stream>>>(p.partial, blocks, d, dwq, dwk);
+  int nq, nk;
+  blocks_for(p.tokens, Hq, Hk, kSms * kPerSm[1], &nq, &nk);
+  k_qk_dw<<<2 * d / 32, 1024, 0, stream>>>(p.partial, nq, nq + nk, d, dwq, dwk);
   return cuda_status(cudaGetLastError());
 }
