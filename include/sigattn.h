@@ -402,7 +402,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  * overlap on the GPU.
  * Errors: INVALID (null pointer, B or N < 1, no heads, norm / interleaved not 0 or 1,
  * negative eps or stride, sections that do not add up, workspace missing or too small),
- * UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past 2^31 - 2^14), ALIGNMENT, CUDA.
+ * UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past 2^31 - 2^14, heads times head stride
+ * past 2^34 elements), ALIGNMENT, CUDA.
  */
 SIGATTN_API int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const int32_t* lengths,
                                      const void* q, const int64_t q_strides[3],

@@ -30,6 +30,7 @@
 #include <cmath>
 
 #include "internal.h"
+#include "sm100.cuh"
 
 namespace sigattn {
 namespace {
@@ -39,15 +40,23 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxAxes = 4;
 // a warp's token index steps past the last one by at most the grid's warps (148 * 3 * 8)
 constexpr int64_t kMaxTokens = 0x7FFFFFFF - 16384;
-constexpr int kDepth = 4;         // steps whose loads are in flight
+constexpr int kDepth = 4;         // slots of a warp: kDepth - 1 steps' loads are in flight
+enum Turn { kNone, kHalves, kPairs };  // rotation: none, halves, pairs side by side
 constexpr int kSms = 148;         // B200
-constexpr int kPerSm[2] = {3, 2};  // resident blocks, forward and backward
+// Resident blocks.  Three pay where a token is one step without angles (single-cell batch,
+// 35.4 us against 37.0); else what every warp does before its first step weighs more (image
+// patches: 38.3 against 34.6), and the backward needs the registers.
+constexpr int per_sm(bool grad, bool turns) { return !grad && !turns ? 3 : 2; }
+constexpr int kGradBlocks = kSms * per_sm(true, true);  // most blocks of a backward
 
 struct QkTensor {
   const uint4* x;
   const uint4* dy;  // backward only
   uint4* y;         // forward: y; backward: dx
-  int64_t x_sb, x_sn, x_sh, dy_sb, dy_sn, dy_sh, y_sb, y_sn, y_sh;  // in 8-value pieces
+  // strides in 8-value pieces; a head's is below 2^31 / H, so that offsets within a token
+  // are 32-bit numbers
+  int64_t x_sb, x_sn, dy_sb, dy_sn, y_sb, y_sn;
+  int x_sh, dy_sh, y_sh;
   const float* w;
   int H;
 };
@@ -68,95 +77,139 @@ struct QkParams {
   float* partial;  // backward: [gridDim.x][d] sums of g u, nullptr without weights
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+// Values travel as pairs of neighbours: the packed fp32 instructions take one issue slot for
+// two, and issue slots are what these kernels run out of before the memory does.
+__device__ __forceinline__ void unpack8(const uint4& v, float2* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// cos and sin of 2 pi turns / 2^32.  The nearest quarter turn is taken off in integers, which
+// leaves an angle of at most pi / 4 for the Taylor polynomials of degree 9 and 8 (remainders
+// below 2e-9 and 3e-8), and decides which of the two is which, and their signs.
+__device__ __forceinline__ void cos_sin(uint32_t turns, float* c, float* s) {
+  const uint32_t quarter = (turns + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(turns - (quarter << 30))) *
+                  (6.283185307179586f * 0x1p-32f);
+  const float q = x * x;
+  float a = fmaf(q, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  a = fmaf(q, a, 1.0f / 120.0f);
+  a = fmaf(q, a, -1.0f / 6.0f);
+  const float sn = fmaf(x * q, a, x);
+  float b = fmaf(q, 1.0f / 40320.0f, -1.0f / 720.0f);
+  b = fmaf(q, b, 1.0f / 24.0f);
+  b = fmaf(q, b, -0.5f);
+  const float cs = fmaf(q, b, 1.0f);
+  const float c0 = quarter & 1 ? sn : cs, s0 = quarter & 1 ? cs : sn;
+  *c = quarter == 1 || quarter == 2 ? -c0 : c0;
+  *s = quarter & 2 ? -s0 : s0;
 }
 
 // What a lane knows of its place in a row: its two pieces and the pairs that they form.
-template <int D>
+template <int D, int TURN>
 struct Lane {
   static constexpr int kLanes = D / 16;      // lanes of a row
   static constexpr int kRows = 32 / kLanes;  // rows of a warp's step
   static constexpr int kOwn = 8 / kRows;     // pairs of the lane's eight that it computes
   int c0, c1;           // pieces
   int sub;              // row of the step
+  bool turn0, turn1;    // whether the pieces' pairs turn
   uint64_t frac[kOwn];  // turns per position of the pairs it computes, in 2^-64
   int axis[kOwn];       // their axes
+  // The token's rotation.  Halves: cosines, sines and negated sines of pairs 2x, 2x + 1.
+  // Side by side: (cos, cos) and (-sin, sin) of pair x.
+  float2 cs[TURN == kPairs ? 8 : 4], sn[TURN == kPairs ? 8 : 4], ms[4];
 
   __device__ Lane(const QkParams& p) {
     const int l = threadIdx.x % 32 % kLanes;
     sub = threadIdx.x % 32 / kLanes;
     const int r = p.rot_dim / 16;  // turned pieces of a half
-    c0 = p.interleaved || l < r ? l : 2 * l;  // halves: behind 2 r pieces the rest pair up
-    c1 = p.interleaved ? l + kLanes : l < r ? l + r : 2 * l + 1;
+    // (halves: behind the 2 r turned pieces the rest follow, so that neighbouring lanes hold
+    // neighbouring pieces and 32-byte sectors are moved whole)
+    c0 = TURN != kHalves || l < r ? l : l + r;
+    c1 = TURN == kHalves && l < r ? l + r : l + kLanes;
+    turn0 = TURN == kPairs ? 8 * c0 < p.rot_dim : l < r;
+    turn1 = TURN == kPairs ? 8 * c1 < p.rot_dim : l < r;
+    if constexpr (TURN != kNone) {
 #pragma unroll
-    for (int x = 0; x < kOwn; ++x) {
-      const int i = sub * kOwn + x;  // of the lane's eight pairs
-      const int pair = !p.interleaved ? 8 * l + i : i < 4 ? 4 * c0 + i : 4 * c1 + i - 4;
-      frac[x] = 0;
-      axis[x] = 0;
-      if (p.interleaved ? 2 * pair < p.rot_dim : l < r) {
-        // inv_freq / 2 pi without its whole turns; scaling by 2^64 is exact
-        double f = p.inv_freq[pair] * 0.15915494309189533577;
-        f -= floor(f);
-        frac[x] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0;
-        while (axis[x] + 1 < p.axes && pair >= p.axis_end[axis[x]]) ++axis[x];
+      for (int x = 0; x < kOwn; ++x) {
+        const int i = sub * kOwn + x;  // of the lane's eight pairs
+        const int pair = TURN == kHalves ? 8 * l + i : i < 4 ? 4 * c0 + i : 4 * c1 + i - 4;
+        frac[x] = 0;
+        axis[x] = 0;
+        if (i < 4 ? turn0 : turn1) {
+          // inv_freq / 2 pi without its whole turns; scaling by 2^64 is exact
+          double f = p.inv_freq[pair] * 0.15915494309189533577;
+          f -= floor(f);
+          frac[x] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0;
+          while (axis[x] + 1 < p.axes && pair >= p.axis_end[axis[x]]) ++axis[x];
+        }
       }
     }
   }
 
-  // cos and sin of the lane's eight angles at the positions pos[axis]
-  __device__ __forceinline__ void angles(const int32_t* pos, float* cs, float* sn) const {
+  // Takes the token's positions pos[axis]; way -1 turns back.
+  __device__ __forceinline__ void place(const int32_t* pos, float way) {
     float c[kOwn], s[kOwn];
 #pragma unroll
     for (int x = 0; x < kOwn; ++x) {
-      const uint64_t turn = frac[x] * static_cast<uint64_t>(static_cast<int64_t>(pos[axis[x]]));
-      // the high word as a signed fraction of half turns in [-1, 1)
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &s[x], &c[x]);
+      const uint64_t turns = frac[x] * static_cast<uint64_t>(static_cast<int64_t>(pos[axis[x]]));
+      cos_sin(static_cast<uint32_t>(turns >> 32), &c[x], &s[x]);
+      s[x] *= way;
     }
     const int l = threadIdx.x % 32 % kLanes;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      cs[j] = __shfl_sync(0xFFFFFFFFu, c[j % kOwn], j / kOwn * kLanes + l);
-      sn[j] = __shfl_sync(0xFFFFFFFFu, s[j % kOwn], j / kOwn * kLanes + l);
+      const float cj = __shfl_sync(0xFFFFFFFFu, c[j % kOwn], j / kOwn * kLanes + l);
+      const float sj = __shfl_sync(0xFFFFFFFFu, s[j % kOwn], j / kOwn * kLanes + l);
+      if constexpr (TURN == kPairs) {
+        cs[j] = both(cj);
+        sn[j] = make_float2(-sj, sj);
+      } else if (j % 2 == 0) {
+        cs[j / 2].x = cj;
+        sn[j / 2].x = sj;
+        ms[j / 2].x = -sj;
+      } else {
+        cs[j / 2].y = cj;
+        sn[j / 2].y = sj;
+        ms[j / 2].y = -sj;
+      }
     }
   }
 
-  // y = R z, or R^T z with the sines negated, on the lane's two pieces z[0..7], z[8..15]
-  __device__ __forceinline__ static void turn(bool interleaved, const float* cs, const float* sn,
-                                              float* z) {
-    if (interleaved) {
+  // z <- R z on the lane's two pieces z[0..3], z[4..7] (pairs of neighbours).  Values outside
+  // the rotation pass untouched: a product with a sine of 0 would spread their infinities.
+  __device__ __forceinline__ void turn(float2* z) const {
+    if constexpr (TURN == kPairs) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = z[2 * j], b = z[2 * j + 1];
-        z[2 * j] = a * cs[j] - b * sn[j];
-        z[2 * j + 1] = a * sn[j] + b * cs[j];
-      }
-    } else {
+      for (int x = 0; x < 2; ++x)
+        if (x == 0 ? turn0 : turn1)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = z[j], b = z[j + 8];
-        z[j] = a * cs[j] - b * sn[j];
-        z[j + 8] = a * sn[j] + b * cs[j];
-      }
+          for (int j = 4 * x; j < 4 * x + 4; ++j)
+            z[j] = fma2(z[j], cs[j], mul2(make_float2(z[j].y, z[j].x), sn[j]));
+    } else if constexpr (TURN == kHalves) {
+      if (turn0)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 a = z[j], b = z[j + 4];
+          z[j] = fma2(a, cs[j], mul2(b, ms[j]));
+          z[j + 4] = fma2(b, cs[j], mul2(a, sn[j]));
+        }
     }
   }
 
   // sum over the lanes of a row
-  __device__ __forceinline__ static float row_sum(float v) {
+  __device__ __forceinline__ static float row_sum(float2 v2) {
+    float v = v2.x + v2.y;
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
@@ -185,29 +238,39 @@ struct Slot {
   int32_t pos[kMaxAxes];
 };
 
-// A warp's walk over the steps of its tokens.
+// A warp's walk over the steps of its tokens: every stride-th token, its heads kRows at a
+// time.  (b, i) move by the stride's whole batch entries and rows, without divisions.
 struct Walk {
-  int tok, h, b, i;  // token, first head of the step, batch entry and row
+  int tok, h, b, i;
   bool valid;
   __device__ __forceinline__ void enter(const QkParams& p) {
-    b = tok / p.N;
-    i = tok - b * p.N;
     valid = tok < p.tokens && (!p.lengths || i < __ldg(p.lengths + b));
   }
-  __device__ __forceinline__ void next(const QkParams& p, int H, int rows, int stride) {
+  __device__ __forceinline__ void next(const QkParams& p, int H, int rows, int stride,
+                                       int stride_b, int stride_i) {
     h += rows;
     if (h >= H) {
       h = 0;
       tok += stride;
-      if (tok < p.tokens) enter(p);
+      b += stride_b;
+      i += stride_i;
+      if (i >= p.N) {
+        i -= p.N;
+        ++b;
+      }
+      enter(p);
     }
+  }
+  // offset of the token in a tensor with these strides, in pieces
+  __device__ __forceinline__ int64_t token(int64_t sb, int64_t sn) const {
+    return b * sb + i * sn;
   }
 };
 
 // Forward (GRAD false) and backward.  In the backward y takes the gradient of x.
-template <int D, bool GRAD>
-__global__ void __launch_bounds__(kThreads, kPerSm[GRAD]) k_qk(const QkParams p) {
-  using L = Lane<D>;
+template <int D, int TURN, bool GRAD>
+__global__ void __launch_bounds__(kThreads, per_sm(GRAD, TURN != kNone)) k_qk(const QkParams p) {
+  using L = Lane<D, TURN>;
   constexpr int kPieces = GRAD ? 4 : 2;
   extern __shared__ uint4 smem[];
   const int warp = threadIdx.x / 32, ln = threadIdx.x % 32;
@@ -216,106 +279,109 @@ __global__ void __launch_bounds__(kThreads, kPerSm[GRAD]) k_qk(const QkParams p)
   const QkTensor& t = p.t[keys];
   const int block = keys ? blockIdx.x - p.blocks0 : blockIdx.x;
   const int stride = (keys ? gridDim.x - p.blocks0 : p.blocks0) * kWarps;
-  const L lane(p);
+  const int stride_b = stride / p.N, stride_i = stride % p.N;
+  L lane(p);
 
-  Walk ahead{block * kWarps + warp, 0, 0, 0, false};
+  const int first = block * kWarps + warp;
+  Walk ahead{first, 0, first / p.N, first % p.N, false};
   ahead.enter(p);
   Walk at = ahead;
+  // the tokens' places in x and dy (ahead) and in y (at), the lane's row in a step
+  int64_t x_at = ahead.token(t.x_sb, t.x_sn), y_at = ahead.token(t.y_sb, t.y_sn);
+  int64_t g_at = GRAD ? ahead.token(t.dy_sb, t.dy_sn) : 0;
   auto fetch = [&](Slot<kPieces>& s) {
     if (ahead.tok < p.tokens) {
       if (ahead.valid) {
         const int h = ahead.h + lane.sub;
         const bool have = h < t.H;
-        const uint4* x = t.x + ahead.b * t.x_sb + ahead.i * t.x_sn + (have ? h : 0) * t.x_sh;
+        const uint4* x = t.x + x_at + (have ? h : 0) * t.x_sh;
         copy16(&s.piece[0][ln], x + lane.c0, have);
         copy16(&s.piece[1][ln], x + lane.c1, have);
         if constexpr (GRAD) {
-          const uint4* g = t.dy + ahead.b * t.dy_sb + ahead.i * t.dy_sn + (have ? h : 0) * t.dy_sh;
+          const uint4* g = t.dy + g_at + (have ? h : 0) * t.dy_sh;
           copy16(&s.piece[2][ln], g + lane.c0, have);
           copy16(&s.piece[3][ln], g + lane.c1, have);
         }
-        if (ahead.h == 0 && ln < p.axes)
+        if (TURN != kNone && ahead.h == 0 && ln < p.axes)
           copy4(&s.pos[ln], p.pos + ln * p.pos_sa + ahead.b * p.pos_sb + ahead.i);
       }
-      ahead.next(p, t.H, L::kRows, stride);
+      ahead.next(p, t.H, L::kRows, stride, stride_b, stride_i);
+      if (ahead.h == 0) {
+        x_at = ahead.token(t.x_sb, t.x_sn);
+        if (GRAD) g_at = ahead.token(t.dy_sb, t.dy_sn);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
   for (int s = 0; s < kDepth - 1; ++s) fetch(slots[s]);
 
-  float w[16], dw[16], cs[8], sn[8];
+  float2 w[8], dw[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    w[j] = t.w ? __ldg(t.w + (j < 8 ? lane.c0 : lane.c1) * 8 + (j & 7)) : 1.0f;
-    dw[j] = 0.0f;
+  for (int j = 0; j < 8; ++j) {
+    const float* at_w = t.w + (j < 4 ? lane.c0 : lane.c1) * 8 + 2 * (j & 3);
+    w[j] = t.w ? make_float2(__ldg(at_w), __ldg(at_w + 1)) : both(1.0f);
+    dw[j] = both(0.0f);
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) cs[j] = 1.0f, sn[j] = 0.0f;
 
-  for (int n = 0; at.tok < p.tokens; ++n) {
-    Slot<kPieces>& s = slots[n % kDepth];
+  for (int n = 0; at.tok < p.tokens; n = n + 1 == kDepth ? 0 : n + 1) {
+    Slot<kPieces>& s = slots[n];
     asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
     const int h = at.h + lane.sub;
     const bool have = h < t.H;
-    uint4* y = t.y + at.b * t.y_sb + at.i * t.y_sn + (have ? h : 0) * t.y_sh;
+    uint4* y = t.y + y_at + (have ? h : 0) * t.y_sh;
+    uint4 out0 = make_uint4(0u, 0u, 0u, 0u), out1 = out0;
     if (at.valid) {
-      if (at.h == 0 && p.rot_dim > 0) {
+      if (TURN != kNone && at.h == 0) {
         __syncwarp();  // the positions were copied by other lanes
-        lane.angles(s.pos, cs, sn);
-        if (GRAD)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
+        lane.place(s.pos, GRAD ? -1.0f : 1.0f);
       }
-      float z[16], g[16];
+      float2 z[8];
       unpack8(s.piece[0][ln], z);
-      unpack8(s.piece[1][ln], z + 8);
-      if constexpr (GRAD) {
-        unpack8(s.piece[2][ln], g);
-        unpack8(s.piece[3][ln], g + 8);
-        L::turn(p.interleaved, cs, sn, g);
-      }
+      unpack8(s.piece[1][ln], z + 4);
       float r = 1.0f;
       if (p.norm) {
-        float sum = 0.0f;
+        float2 sum = mul2(z[0], z[0]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum = fmaf(z[j], z[j], sum);
+        for (int j = 1; j < 8; ++j) sum = fma2(z[j], z[j], sum);
         r = rsqrtf(fmaf(L::row_sum(sum), p.inv_d, p.eps));
       }
       if constexpr (!GRAD) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] *= r * w[j];
-        L::turn(p.interleaved, cs, sn, z);
-        if (have) {
-          y[lane.c0] = pack8(z);
-          y[lane.c1] = pack8(z + 8);
-        }
+        for (int j = 0; j < 8; ++j) z[j] = mul2(mul2(z[j], both(r)), w[j]);
+        lane.turn(z);
+        out0 = pack8(z);
+        out1 = pack8(z + 4);
       } else {
+        float2 g[8];
+        unpack8(s.piece[2][ln], g);
+        unpack8(s.piece[3][ln], g + 4);
+        lane.turn(g);
         // a lane without a row has u = g = 0 and, with r = 0 (not rsqrt(eps)), adds nothing
         if (!have) r = 0.0f;
-        float dot = 0.0f;
+        float2 dot = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          z[j] *= r;
-          dw[j] = fmaf(g[j], z[j], dw[j]);
-          g[j] *= w[j];
-          dot = fmaf(g[j], z[j], dot);
+        for (int j = 0; j < 8; ++j) {
+          z[j] = mul2(z[j], both(r));
+          dw[j] = fma2(g[j], z[j], dw[j]);
+          g[j] = mul2(g[j], w[j]);
+          dot = fma2(g[j], z[j], dot);
         }
-        dot = p.norm ? L::row_sum(dot) * p.inv_d : 0.0f;
+        const float mean = p.norm ? -L::row_sum(dot) * p.inv_d : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) g[j] = r * fmaf(-z[j], dot, g[j]);
-        if (have) {
-          y[lane.c0] = pack8(g);
-          y[lane.c1] = pack8(g + 8);
-        }
+        for (int j = 0; j < 8; ++j) g[j] = mul2(fma2(z[j], both(mean), g[j]), both(r));
+        out0 = pack8(g);
+        out1 = pack8(g + 4);
       }
-    } else if (have) {
-      y[lane.c0] = make_uint4(0u, 0u, 0u, 0u);
-      y[lane.c1] = make_uint4(0u, 0u, 0u, 0u);
     }
-    at.next(p, t.H, L::kRows, stride);
-    __syncwarp();  // every lane has read the positions of the slot that is filled next
-    fetch(slots[(n + kDepth - 1) % kDepth]);
+    if (have) {
+      y[lane.c0] = out0;
+      y[lane.c1] = out1;
+    }
+    at.next(p, t.H, L::kRows, stride, stride_b, stride_i);
+    if (at.h == 0) y_at = at.token(t.y_sb, t.y_sn);
+    if (TURN != kNone) __syncwarp();  // every lane has read the positions of the next slot
+    fetch(slots[n == 0 ? kDepth - 1 : n - 1]);
   }
   if (!GRAD || !p.partial) return;
   // The block's sums, in a fixed order: the rows of each warp by shuffles, the warps one
@@ -323,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm[GRAD]) k_qk(const QkParams p)
   __shared__ float sums[kWarps][D];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    float v = dw[j];
+    float v = j % 2 ? dw[j / 2].y : dw[j / 2].x;
 #pragma unroll
     for (int o = 16; o >= L::kLanes; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (lane.sub == 0) sums[warp][(j < 8 ? lane.c0 : lane.c1) * 8 + (j & 7)] = v;
@@ -349,9 +415,16 @@ __global__ void __launch_bounds__(1024) k_qk_dw(const float* __restrict__ partia
   const int c0 = (blockIdx.x % (d / 32)) * 32;
   float* out = keys ? dwk : dwq;
   if (!out) return;
-  float v = 0.0f;
-  for (int r = (keys ? rows0 : 0) + warp; r < (keys ? rows : rows0); r += 32)
-    v += partial[r * d + c0 + lane];
+  constexpr int kMost = (kGradBlocks + 1 + 31) / 32;  // rows of a warp, all read at once
+  const int end = keys ? rows : rows0;
+  float in[kMost], v = 0.0f;
+#pragma unroll
+  for (int x = 0; x < kMost; ++x) {
+    const int r = (keys ? rows0 : 0) + warp + 32 * x;
+    in[x] = r < end ? partial[r * d + c0 + lane] : 0.0f;
+  }
+#pragma unroll
+  for (int x = 0; x < kMost; ++x) v += in[x];
   sums[warp][lane] = v;
   __syncthreads();
   v = sums[lane][warp];
@@ -361,29 +434,45 @@ __global__ void __launch_bounds__(1024) k_qk_dw(const float* __restrict__ partia
 }
 
 // Blocks of the queries and of the keys: a warp per token of each, or as many as the GPU
-// holds at once, shared out by their heads.
-void blocks_for(int tokens, int Hq, int Hk, int most, int* q, int* k) {
-  const int need = (tokens + kWarps - 1) / kWarps;
-  const int64_t heads = static_cast<int64_t>(Hq) + Hk;
-  *q = Hq == 0 ? 0 : std::max<int>(1, std::min<int64_t>(need, static_cast<int64_t>(most) * Hq / heads));
-  *k = Hk == 0 ? 0 : std::max<int>(1, std::min<int64_t>(need, static_cast<int64_t>(most) * Hk / heads));
+// holds at once, shared out by the work of a token: its steps, and about one more for the
+// angles (by heads alone, 4 key heads beside 16 query heads took a third longer than these).
+void blocks_for(const QkParams& p, bool grad, int* q, int* k) {
+  const int Hq = p.t[0].H, Hk = p.t[1].H;
+  const int need = (p.tokens + kWarps - 1) / kWarps;
+  const int rows = 512 / p.d, more = p.rot_dim > 0 ? 1 : 0;
+  const int64_t wq = Hq == 0 ? 0 : (Hq + rows - 1) / rows + more;
+  const int64_t wk = Hk == 0 ? 0 : (Hk + rows - 1) / rows + more;
+  const int64_t most = kSms * per_sm(grad, p.rot_dim > 0);
+  *q = Hq == 0 ? 0 : std::max<int>(1, std::min<int64_t>(need, most * wq / (wq + wk)));
+  *k = Hk == 0 ? 0 : std::max<int>(1, std::min<int64_t>(need, most * wk / (wq + wk)));
 }
 
-template <int D, bool GRAD>
-int launch_qk(QkParams& p, cudaStream_t stream) {
+template <int D, int TURN, bool GRAD>
+int launch_turn(const QkParams& p, int blocks, cudaStream_t stream) {
   constexpr int bytes = kWarps * kDepth * sizeof(Slot<GRAD ? 4 : 2>);
-  int q, k;
-  blocks_for(p.tokens, p.t[0].H, p.t[1].H, kSms * kPerSm[GRAD], &q, &k);
-  p.blocks0 = q;
-  const auto kern = k_qk<D, GRAD>;
+  const auto kern = k_qk<D, TURN, GRAD>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return cuda_status(e);
-  kern<<<q + k, kThreads, bytes, stream>>>(p);
+  kern<<<blocks, kThreads, bytes, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
-int check_strided(const void* ptr, const int64_t* strides, int64_t s[3]) {
+template <bool GRAD>
+int launch_qk(QkParams& p, cudaStream_t stream) {
+  int q, k;
+  blocks_for(p, GRAD, &q, &k);
+  p.blocks0 = q;
+  if (p.d == 64)
+    return p.rot_dim == 0  ? launch_turn<64, kNone, GRAD>(p, q + k, stream)
+           : p.interleaved ? launch_turn<64, kPairs, GRAD>(p, q + k, stream)
+                           : launch_turn<64, kHalves, GRAD>(p, q + k, stream);
+  return p.rot_dim == 0  ? launch_turn<128, kNone, GRAD>(p, q + k, stream)
+         : p.interleaved ? launch_turn<128, kPairs, GRAD>(p, q + k, stream)
+                         : launch_turn<128, kHalves, GRAD>(p, q + k, stream);
+}
+
+int check_strided(const void* ptr, const int64_t* strides, int H, int64_t s[3]) {
   if (!ptr || !strides) return SIGATTN_ERR_INVALID;
   for (int i = 0; i < 3; ++i)
     if (strides[i] < 0) return SIGATTN_ERR_INVALID;
@@ -392,6 +481,7 @@ int check_strided(const void* ptr, const int64_t* strides, int64_t s[3]) {
     if (strides[i] % 8 != 0) return SIGATTN_ERR_ALIGNMENT;
     s[i] = strides[i] / 8;
   }
+  if (s[2] > 0x7FFFFFFF / H) return SIGATTN_ERR_UNSUPPORTED;
   return SIGATTN_OK;
 }
 
@@ -446,17 +536,17 @@ int check_one(int H, const void* x, const int64_t* xs, const void* dy, const int
   if (H == 0) return SIGATTN_OK;
   int64_t s[3];
   int rc;
-  if ((rc = check_strided(x, xs, s)) != SIGATTN_OK) return rc;
+  if ((rc = check_strided(x, xs, H, s)) != SIGATTN_OK) return rc;
   t->x = static_cast<const uint4*>(x);
-  t->x_sb = s[0], t->x_sn = s[1], t->x_sh = s[2];
+  t->x_sb = s[0], t->x_sn = s[1], t->x_sh = static_cast<int>(s[2]);
   if (grad) {
-    if ((rc = check_strided(dy, dys, s)) != SIGATTN_OK) return rc;
+    if ((rc = check_strided(dy, dys, H, s)) != SIGATTN_OK) return rc;
     t->dy = static_cast<const uint4*>(dy);
-    t->dy_sb = s[0], t->dy_sn = s[1], t->dy_sh = s[2];
+    t->dy_sb = s[0], t->dy_sn = s[1], t->dy_sh = static_cast<int>(s[2]);
   }
-  if ((rc = check_strided(y, ys, s)) != SIGATTN_OK) return rc;
+  if ((rc = check_strided(y, ys, H, s)) != SIGATTN_OK) return rc;
   t->y = static_cast<uint4*>(y);
-  t->y_sb = s[0], t->y_sn = s[1], t->y_sh = s[2];
+  t->y_sb = s[0], t->y_sn = s[1], t->y_sh = static_cast<int>(s[2]);
   t->w = w;
   return SIGATTN_OK;
 }
@@ -485,8 +575,7 @@ extern "C" int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const i
   if ((rc = check_one(Hk, k, k_strides, nullptr, nullptr, false, yk, yk_strides, wk, &p.t[1])) !=
       SIGATTN_OK)
     return rc;
-  const cudaStream_t stream = static_cast<cudaStream_t>(s);
-  return d == 64 ? launch_qk<64, false>(p, stream) : launch_qk<128, false>(p, stream);
+  return launch_qk<false>(p, static_cast<cudaStream_t>(s));
 }
 
 extern "C" int sigattn_qk_norm_rope_bwd_workspace_size(int B, int N, int d, size_t* bytes) {
@@ -495,7 +584,7 @@ extern "C" int sigattn_qk_norm_rope_bwd_workspace_size(int B, int N, int d, size
     return SIGATTN_ERR_UNSUPPORTED;
   // of any head counts: the queries' and the keys' blocks, one more where a share rounds up
   const size_t most = std::min<size_t>(2 * ((static_cast<size_t>(B) * N + kWarps - 1) / kWarps),
-                                       kSms * kPerSm[1] + 1);
+                                       kGradBlocks + 1);
   *bytes = sizeof(float) * d * most;
   return SIGATTN_OK;
 }
@@ -528,10 +617,10 @@ extern "C" int sigattn_qk_norm_rope_bwd(
     p.partial = static_cast<float*>(workspace);
   }
   const cudaStream_t stream = static_cast<cudaStream_t>(s);
-  rc = d == 64 ? launch_qk<64, true>(p, stream) : launch_qk<128, true>(p, stream);
+  rc = launch_qk<true>(p, stream);
   if (rc != SIGATTN_OK || !p.partial) return rc;
   int nq, nk;
-  blocks_for(p.tokens, Hq, Hk, kSms * kPerSm[1], &nq, &nk);
+  blocks_for(p, true, &nq, &nk);
   k_qk_dw<<<2 * d / 32, 1024, 0, stream>>>(p.partial, nq, nq + nk, d, dwq, dwk);
   return cuda_status(cudaGetLastError());
 }
