@@ -140,7 +140,7 @@ __global__ void k_wait_selftest(int* status, unsigned long long limit_ns) {
 
 unsigned long long wait_limit_ns() { return g_wait_limit_ns.load(); }
 
-int make_tmap_bf16(CUtensorMap* map, const TensorDesc& t, int B, int H, int d) {
+int make_tmap_bf16(CUtensorMap* map, const TensorDesc& t, int B, int H, int d, int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return SIGATTN_ERR_CUDA;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(t.N),
@@ -148,7 +148,7 @@ int make_tmap_bf16(CUtensorMap* map, const TensorDesc& t, int B, int H, int d) {
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t.sn) * 2,
                                  static_cast<cuuint64_t>(t.sh) * 2,
                                  static_cast<cuuint64_t>(t.sb) * 2};
-  const cuuint32_t box[4] = {64, 128, 1, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.ptr), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -111,8 +111,8 @@ struct TensorDesc {
 };
 
 // Builds a 4-D TMA descriptor over a [B, N, H, d] bf16 tensor with a box of
-// 64 (d) x 128 (tokens) x 1 x 1 and 128-byte swizzle.
-int make_tmap_bf16(CUtensorMap* map, const TensorDesc& t, int B, int H, int d);
+// 64 (d) x 128 (tokens; or `rows`) x 1 x 1 and 128-byte swizzle.
+int make_tmap_bf16(CUtensorMap* map, const TensorDesc& t, int B, int H, int d, int rows = 128);
 
 // 4-D TMA descriptor over a contiguous fp32 [B, N, H, d] tensor with a box of 32 (d) x 16
 // (tokens) x 1 x 1 and 128-byte swizzle (the fused backward's dQ accumulator).

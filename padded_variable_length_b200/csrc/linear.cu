@@ -35,14 +35,16 @@ constexpr int kChunk = 128;
 constexpr int kCols = 64;       // value columns of a work item
 constexpr int kSms = 148;       // B200
 constexpr int kMaxSorted = 512;  // batches up to this size are walked longest-first
-constexpr int kThreads = 512;
-constexpr int kWarpP = 4, kWarpV = 8, kWarpS = 12;  // first warps of the three warpgroups
+constexpr int kThreads = 576;
+// first warps of P, V', the outputs and the state, four each
+constexpr int kWarpP = 2, kWarpV = 6, kWarpO = 10, kWarpS = 14;
 
 struct LinPass {
   int q, k, v;     // which of the tensor maps stand in the places of q, k, v
   int reverse;
   float o1, o2;    // factors of Q R and of P V in the output
   float vs;        // factor of V' (what the state accumulates)
+  int o;           // tensor map of the output
   __nv_bfloat16* out;
   int64_t o_sb, o_sn, o_sh;
   const float* init;    // state before the first chunk, nullptr: 0; element (row, col) of
@@ -52,7 +54,7 @@ struct LinPass {
 };
 
 struct LinParams {
-  CUtensorMap map[4];
+  CUtensorMap map[7];  // inputs (boxes of 128 rows), then outputs (32 rows)
   LinPass pass[3];
   int npass, B, H, N, T, nseg, seg_chunks, nitems;
   const int32_t* lengths;
@@ -124,45 +126,144 @@ __device__ __forceinline__ int valid_of(const Item& it, int c) {
   return min(kChunk, it.s.n - c * kChunk);
 }
 
-template <int D, bool HILO>
+template <int D>
 struct LinLayout {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBox = 128 * 128;            // 128 tokens x 64 bf16
   static constexpr int kTile = kBoxes * kBox;       // a Q or K tile
   static constexpr int kSt = D == 64 ? 3 : 2;       // stages of Q and K
-  static constexpr int kVs = D == 64 ? 4 : 3;       // stages of V
+  static constexpr int kVs = D == 64 ? 4 : 2;       // stages of V
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + kSt * kTile;
   static constexpr int kV = kK + kSt * kTile;
-  static constexpr int kVp = kV + kVs * kBox;       // V' (and its rounding error, HILO)
-  static constexpr int kR = kVp + (HILO ? 2 : 1) * kBox;  // bf16 state, D rows of 64
-  static constexpr int kBar = kR + D * 128;
-  // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2] u_full[2]
-  // u_empty[2] vp_full r_full o_empty done
-  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 12;
+  static constexpr int kVp = kV + kVs * kBox;       // V' and, behind it, its rounding error
+  static constexpr int kR = kVp + 2 * kBox;         // bf16 state, D rows of 64
+  static constexpr int kO = kR + D * 128;           // outputs on their way, 4 KB per warp
+  static constexpr int kBar = kO + kBox;
+  // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2] u_full u_empty
+  // vp_full r_full o_empty done
+  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 10;
   static constexpr int kMisc = kBar + 8 * kNumBars;  // tmem base, abort, drain flags
-  static constexpr int kOrder = kMisc + 16;
+  static constexpr int kPow = kMisc + 16;            // powers of lambda, 32 per warp of P
+  static constexpr int kOrder = kPow + 4 * 32 * 4;
   static constexpr int kBytes = kOrder + 2 * kMaxSorted;
   static constexpr int kAlloc = kBytes + 1024;       // slack for 1024-byte alignment
   // TMEM columns
   static constexpr int kTS = 0;     // two S / P buffers of 128
   static constexpr int kTO1 = 256;  // Q R
   static constexpr int kTO2 = 320;  // P V
-  static constexpr int kTU = 384;   // two K^T V' buffers of 64
+  static constexpr int kTU = 384;   // K^T V', then K^T times its rounding error
 };
+
+// Products of a chunk with the commit behind them, all issued under one elect.sync (see
+// mma_ss_lh_w): these loops are unrolled in full, and four roles' code has to stay in the
+// instruction cache together, so a product is kept to a handful of instructions.
+#define SIGATTN_LIN_STEP(OA, OB)                                               \
+  "add.u32 la, %1, " #OA ";\n\tadd.u32 lb, %2, " #OB ";\n\t"                   \
+  "mov.b64 da, {la, %3};\n\tmov.b64 db, {lb, %3};\n\t"                        \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, q;\n\t"
+#define SIGATTN_LIN_HEAD                                                        \
+  "{\n\t.reg .pred p, q, e;\n\t.reg .b64 da, db;\n\t.reg .b32 la, lb;\n\t"     \
+  "setp.ne.b32 p, %6, 1;\n\tsetp.ne.b32 q, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t" \
+  "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"                        \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t"
+#define SIGATTN_LIN_TAIL \
+  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}\n"
+
+// D = Q R: A K-major (32 bytes a step, boxes of 64 columns), B MN-major (2048 bytes a step).
+template <int kSteps>
+__device__ __forceinline__ void mma_qr_commit_w(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                uint32_t hi, uint32_t idesc, uint64_t* bar) {
+  static_assert(kSteps == 4 || kSteps == 8, "d = 64 or 128");
+  if constexpr (kSteps == 4) {
+    asm volatile(SIGATTN_LIN_HEAD SIGATTN_LIN_STEP(2, 128) SIGATTN_LIN_STEP(4, 256)
+                     SIGATTN_LIN_STEP(6, 384) SIGATTN_LIN_TAIL ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(smem_u32(bar)), "r"(1u)
+                 : "memory");
+  } else {
+    asm volatile(SIGATTN_LIN_HEAD SIGATTN_LIN_STEP(2, 128) SIGATTN_LIN_STEP(4, 256)
+                     SIGATTN_LIN_STEP(6, 384) SIGATTN_LIN_STEP(1024, 512)
+                         SIGATTN_LIN_STEP(1026, 640) SIGATTN_LIN_STEP(1028, 768)
+                             SIGATTN_LIN_STEP(1030, 896) SIGATTN_LIN_TAIL ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(smem_u32(bar)), "r"(1u)
+                 : "memory");
+  }
+}
+
+// D = K^T V' over 128 tokens: A and B MN-major, 16 tokens (2048 bytes) a step.
+__device__ __forceinline__ void mma_kv_commit_w(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                                uint32_t hi, uint32_t idesc, uint64_t* bar) {
+  asm volatile(SIGATTN_LIN_HEAD SIGATTN_LIN_STEP(128, 128) SIGATTN_LIN_STEP(256, 256)
+                   SIGATTN_LIN_STEP(384, 384) SIGATTN_LIN_STEP(512, 512)
+                       SIGATTN_LIN_STEP(640, 640) SIGATTN_LIN_STEP(768, 768)
+                           SIGATTN_LIN_STEP(896, 896) SIGATTN_LIN_TAIL ::"r"(d_tmem),
+               "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(smem_u32(bar)), "r"(1u)
+               : "memory");
+}
+#undef SIGATTN_LIN_STEP
+#undef SIGATTN_LIN_HEAD
+#undef SIGATTN_LIN_TAIL
+
+// 16 columns from c0 of row i of S, weighted by lambda^|i - j|, masked and rounded.  pow: the
+// powers of lambda over 32 columns, see the caller.
+__device__ __forceinline__ void weigh(const uint32_t (&s)[16], int c0, int m, bool rev, int i,
+                                      float l2, const float* pow, uint32_t (&pk)[8]) {
+  const int at = c0 - i;      // j - i of the first column
+  const int last = m - c0;    // columns from here on are behind the sequence
+  if (c0 / 32 != i / 32) {
+    const int blk = c0 & ~31;
+    const float f = ex2_approx(l2 * static_cast<float>(rev ? blk - i : i - blk - 31));
+    const float2 f2 = make_float2(f, f);
+    float v[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(s[c]);
+    if (rev && last < 16) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) v[c] = c < last ? v[c] : 0.0f;
+    }
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(pow + (c0 & 16) + c);
+      const float2 a = mul2(mul2(make_float2(v[c], v[c + 1]), f2), make_float2(q.x, q.y));
+      const float2 b = mul2(mul2(make_float2(v[c + 2], v[c + 3]), f2), make_float2(q.z, q.w));
+      pk[c / 2] = pack_bf16x2(a.x, a.y);
+      pk[c / 2 + 1] = pack_bf16x2(b.x, b.y);
+    }
+  } else {
+    const float x0 = l2 * static_cast<float>(rev ? at : -at), dx = rev ? l2 : -l2;
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      float f[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const bool keep = rev ? at + c + y >= 0 && c + y < last : at + c + y <= 0;
+        const float x = ex2_approx(fmaf(dx, static_cast<float>(c + y), x0));
+        f[y] = keep ? __uint_as_float(s[c + y]) * x : 0.0f;
+      }
+      pk[c / 2] = pack_bf16x2(f[0], f[1]);
+    }
+  }
+}
 
 // OUT: the whole computation.  Otherwise only the state that each segment of a sequence
 // leaves from a zero start is computed, into pass.seg.
-// HILO: V' as the sum of two bf16 values (relative error 2^-18 instead of 2^-9), for the
-// calls that hand the fp32 state to the user; the outputs in bf16 do not need it.
-template <int D, bool OUT, bool HILO>
+//
+// Warps: 0 copies, 1 issues the products, then four jobs on a chunk, each with warps of its
+// own so that none waits for another's turn:
+//   P       S from TMEM, decayed, masked and rounded into the A operand of P V
+//   V'      the decayed values, as the sum of two bf16 numbers: rounded once they would cost
+//           the outputs a third rounding (2.6e-3 off instead of 2.3e-3, where one rounding is
+//           1.7e-3) and the fp32 states their accuracy (2^-9 instead of 2^-18)
+//   O       lambda^(i+1) Q R + P V to bf16 and out, a tensor-map store of 32 rows per warp
+//   state   R <- lambda^m R + K^T V' in registers; its bf16 copy is the B operand of Q R
+template <int D, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinParams p) {
-  using L = LinLayout<D, HILO>;
+  using L = LinLayout<D>;
   constexpr int ST = L::kSt, VS = L::kVs;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  // (an offset, not a cast of the rounded address, which would lose its address space)
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const int warp = warp_id(), lane = lane_id();
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kBar);
   uint64_t* qk_full = bars;
@@ -172,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = pv_done + VS;
   uint64_t* p_full = s_full + 2;
   uint64_t* u_full = p_full + 2;       // K^T V' complete: U ready, V' free
-  uint64_t* u_empty = u_full + 2;
-  uint64_t* vp_full = u_empty + 2;
+  uint64_t* u_empty = u_full + 1;
+  uint64_t* vp_full = u_empty + 1;
   uint64_t* r_full = vp_full + 1;
   uint64_t* o_empty = r_full + 1;
   uint64_t* done = o_empty + 1;
@@ -195,9 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
-      mbar_init(u_full + i, 1);
-      mbar_init(u_empty + i, 4);
     }
+    mbar_init(u_full, 1);
+    mbar_init(u_empty, 4);
     mbar_init(vp_full, 4);
     mbar_init(r_full, 4);
     mbar_init(o_empty, 4);
@@ -274,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kHi = sw128_desc_hi(1024);
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, kCols, true);
-    constexpr uint32_t idesc_u = idesc_bf16_f32(128, kCols, true, true);
+    constexpr uint32_t idesc_u = idesc_bf16_f32(128, 2 * kCols, true, true);
     int total = 0;
     for (int k = 0;; ++k) {
       const int w = snake_item(k);
@@ -290,14 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     while ((OUT ? tp : tu) < total) {
       bool progress = false;
       if (OUT && tp < to && ready(p_full + (tp & 1), tp >> 1)) {
-        // O2 = P V (P from TMEM, 16 keys in 8 columns)
+        // O2 = P V (P from TMEM)
         tc_fence_after();
         const uint32_t v_base = smem_u32(smem + L::kV + (tp % VS) * L::kBox);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts_lh_w(tmem + L::kTO2, tmem + L::kTS + (tp & 1) * 128 + kk * 8,
-                      sw128_desc_lo(v_base + kk * 2048, L::kBox), kHi, idesc_o, kk > 0);
-        mma_commit_w(pv_done + tp % VS);
+        mma_pv8_commit_w(tmem + L::kTO2, tmem + L::kTS + (tp & 1) * 128,
+                         sw128_desc_lo(v_base, L::kBox), kHi, idesc_o, 0u, pv_done + tp % VS);
         ++tp;
         progress = true;
       }
@@ -306,32 +404,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t q_base = smem_u32(smem + L::kQ + (to % ST) * L::kTile);
         const uint32_t r_base = smem_u32(smem + L::kR);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss_lh_w(tmem + L::kTO1,
-                      sw128_desc_lo(q_base + (kk >> 2) * L::kBox + (kk & 3) * 32, 16),
-                      sw128_desc_lo(r_base + kk * 2048, L::kBox), kHi, idesc_o, kk > 0);
-        mma_commit_w(qk_empty + to % ST);
+        mma_qr_commit_w<D / 16>(tmem + L::kTO1, sw128_desc_lo(q_base, 16),
+                                sw128_desc_lo(r_base, L::kBox), kHi, idesc_o,
+                                qk_empty + to % ST);
         ++to;
         progress = true;
       }
-      if (tu < (OUT ? ts : total) && ready(vp_full, tu) &&
-          (tu < 2 || ready(u_empty + (tu & 1), (tu >> 1) - 1)) &&
+      if (tu < (OUT ? ts : total) && ready(vp_full, tu) && (tu == 0 || ready(u_empty, tu - 1)) &&
           (OUT || ready(qk_full + tu % ST, tu / ST))) {
-        // U = K^T V'.  A holds the K columns as rows: 128 for d = 128; for d = 64 the chunk
-        // stride of 0 gives them twice, lanes 64-127 a copy of lanes 0-63.
+        // U = K^T (V' | its rounding error).  A holds the K columns as rows: 128 for d = 128;
+        // for d = 64 the chunk stride of 0 gives them twice, lanes 64-127 a copy of 0-63.
         tc_fence_after();
         const uint32_t k_base = smem_u32(smem + L::kK + (tu % ST) * L::kTile);
         const uint32_t v_base = smem_u32(smem + L::kVp);
-#pragma unroll
-        for (int x = 0; x < (HILO ? 2 : 1); ++x)
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss_lh_w(tmem + L::kTU + (tu & 1) * 64,
-                        sw128_desc_lo(k_base + kk * 2048, D == 128 ? L::kBox : 0),
-                        sw128_desc_lo(v_base + x * L::kBox + kk * 2048, L::kBox), kHi, idesc_u,
-                        x + kk > 0);
-        mma_commit_w(u_full + (tu & 1));
+        mma_kv_commit_w(tmem + L::kTU, sw128_desc_lo(k_base, D == 128 ? L::kBox : 0),
+                        sw128_desc_lo(v_base, L::kBox), kHi, idesc_u, u_full);
         if (!OUT) {
           mma_commit_w(qk_empty + tu % ST);
           mma_commit_w(pv_done + tu % VS);
@@ -344,13 +431,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t q_base = smem_u32(smem + L::kQ + (ts % ST) * L::kTile);
         const uint32_t k_base = smem_u32(smem + L::kK + (ts % ST) * L::kTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * L::kBox + (kk & 3) * 32;
-          mma_ss_lh_w(tmem + L::kTS + (ts & 1) * 128, sw128_desc_lo(q_base + off, 16),
-                      sw128_desc_lo(k_base + off, 16), kHi, idesc_s, kk > 0);
-        }
-        mma_commit_w(s_full + (ts & 1));
+        mma_s_commit_w<D / 16>(tmem + L::kTS + (ts & 1) * 128, sw128_desc_lo(q_base, 16),
+                               sw128_desc_lo(k_base, 16), kHi, idesc_s, s_full + (ts & 1));
         ++ts;
         progress = true;
       }
@@ -369,28 +451,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(done);
     const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
     mbar_wait_w(done, 0, drain);
-  } else if (warp < kWarpP) {
-    // ---------------------------------------------------------------- zero rows
-    // Rows behind a padded sequence, within the item's segment, are written as 0.
-    if (OUT && !p.cu) {
-      for (int k = 0;; ++k) {
-        const int w = snake_item(k);
-        if (w >= p.nitems) break;
-        const Item it = decode<D>(p, order, w);
-        const LinPass& ps = p.pass[it.pass];
-        const int lo = it.c0 * kChunk;
-        const int hi = it.seg == p.nseg - 1 ? p.N : min(p.N, lo + p.seg_chunks * kChunk);
-        __nv_bfloat16* out = ps.out + it.b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols;
-        for (int r = max(lo, it.s.n) + (warp - 2) * 4 + lane / 8; r < hi; r += 8)
-          *reinterpret_cast<uint4*>(out + r * ps.o_sn + (lane % 8) * 8) =
-              make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
   } else if (warp < kWarpV) {
     // ---------------------------------------------------------------- P = decayed, masked S
+    // lambda^|i - j| in blocks of 32 columns: off the diagonal the product of a row's power up
+    // to the block's near end and a column's power from there, both at most 1 for any decay;
+    // in the diagonal block, where that split would overflow, exp2 of each element.
     if (OUT) {
       const int wq = warp & 3, i = wq * 32 + lane;
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+      float* pow = reinterpret_cast<float*>(smem + L::kPow) + wq * 32;
       int t = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {
@@ -399,35 +468,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item it = decode<D>(p, order, w);
         const bool rev = p.pass[it.pass].reverse != 0;
         const float l2 = clamped_decay(p, it.h) * kLog2e;
+        __syncwarp();
+        pow[lane] = ex2_approx(l2 * static_cast<float>(rev ? lane : 31 - lane));
+        __syncwarp();
         for (int j = 0; j < it.cn; ++j, ++t) {
           const int m = valid_of(it, chunk_of(it, rev, j));
           const uint32_t sb = t_lane + L::kTS + (t & 1) * 128;
           if (!(ok = mbar_wait_w(s_full + (t & 1), (t >> 1) & 1, wctx))) break;
           tc_fence_after();
+          uint32_t pk[8];
+          // Columns [first, end) have kept elements, 16 at a time; P of keys c0.. goes to
+          // column (c0 / 64) 64 + (c0 % 64) / 2, where S has been read by then.
+          const int first = rev ? wq * 32 : 0, end = rev ? 128 : wq * 32 + 32;
 #pragma unroll 1
-          for (int blk = 0; blk < 4; ++blk) {
-            uint32_t pk[16];
-            if (rev ? blk < wq : blk > wq) {
+          for (int c0 = 0; c0 < 128; c0 += 16) {
+            const uint32_t dst = sb + (c0 & 64) + (c0 & 63) / 2;
+            if (c0 < first || c0 >= end) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) pk[c] = 0u;
+              for (int c = 0; c < 8; ++c) pk[c] = 0u;
             } else {
-              uint32_t sr[32];
-              tmem_ld32(sb + blk * 32, sr);
+              uint32_t sr[16];
+              tmem_ld16(sb + c0, sr);
               tmem_wait_ld();
-              // lambda^|i - j|: j = 32 blk + c, so l2 |i - j| = x0 -+ l2 c
-              const int at = blk * 32 - i;  // j - i of the block's first column
-              const float x0 = l2 * static_cast<float>(rev ? at : -at), dx = rev ? l2 : -l2;
-              float f[32];
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                const bool keep = rev ? (at + c >= 0 && blk * 32 + c < m) : at + c <= 0;
-                const float x = ex2_approx(fmaf(dx, static_cast<float>(c), x0));
-                f[c] = keep ? __uint_as_float(sr[c]) * x : 0.0f;
-              }
-#pragma unroll
-              for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(f[2 * c], f[2 * c + 1]);
+              weigh(sr, c0, m, rev, i, l2, pow, pk);
             }
-            tmem_st16(sb + blk * 16, pk);
+            tmem_st8(dst, pk);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -436,43 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < kWarpS) {
-    // ---------------------------------------------------------------- V' and the outputs
-    const int wq = warp & 3, tid = threadIdx.x - kWarpV * 32;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const int i = wq * 32 + lane;
+  } else if (warp < kWarpO) {
+    // ---------------------------------------------------------------- V'
+    const int tid = threadIdx.x - kWarpV * 32;
     int t = 0;
     bool ok = true;
-    // the chunk whose outputs are still to be written
-    __nv_bfloat16* o_row = nullptr;
-    float o_f1 = 0.0f, o_f2 = 0.0f;
-    auto write_out = [&](int to) -> bool {
-      if (!mbar_wait_w(pv_done + to % VS, (to / VS) & 1, wctx)) return false;
-      tc_fence_after();
-      uint32_t pk[32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t a[16], b[16];
-        tmem_ld16(t_lane + L::kTO1 + c * 16, a);
-        tmem_ld16(t_lane + L::kTO2 + c * 16, b);
-        tmem_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          pk[c * 8 + x] = pack_bf16x2(
-              fmaf(o_f1, __uint_as_float(a[2 * x]), o_f2 * __uint_as_float(b[2 * x])),
-              fmaf(o_f1, __uint_as_float(a[2 * x + 1]), o_f2 * __uint_as_float(b[2 * x + 1])));
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_empty);
-      if (o_row) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          reinterpret_cast<uint4*>(o_row)[c] =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-      }
-      return true;
-    };
     for (int k = 0; ok; ++k) {
       const int w = snake_item(k);
       if (w >= p.nitems) break;
@@ -481,65 +514,153 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool rev = ps.reverse != 0;
       const float l2 = clamped_decay(p, it.h) * kLog2e;
       for (int j = 0; j < it.cn; ++j, ++t) {
-        const int c = chunk_of(it, rev, j), m = valid_of(it, c);
+        const int m = valid_of(it, chunk_of(it, rev, j));
         const int vs = t % VS, s = t % ST;
         if (!(ok = mbar_wait_w(v_full + vs, (t / VS) & 1, wctx))) break;
         if (m < kChunk && !(ok = mbar_wait_w(qk_full + s, (t / ST) & 1, wctx))) break;
-        if (t > 0 && !(ok = mbar_wait_w(u_full + ((t - 1) & 1), ((t - 1) >> 1) & 1, wctx))) break;
-        uint8_t* v = smem + L::kV + vs * L::kBox;
-        uint8_t* vp = smem + L::kVp;
-        // 16 bytes a step, at the address they have in the swizzled tile: its row is what
-        // counts
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int off = (tid + x * 128) * 16, row = off / 128;
-          uint4 in = *reinterpret_cast<const uint4*>(v + off);
-          const float f =
-              ps.vs * ex2_approx(l2 * static_cast<float>(rev ? row + 1 : m - 1 - row));
-          uint32_t hi[4], lo[4];
-          const uint32_t wds[4] = {in.x, in.y, in.z, in.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float a = __uint_as_float(wds[y] << 16) * f;
-            const float b = __uint_as_float(wds[y] & 0xFFFF0000u) * f;
-            hi[y] = pack_bf16x2(a, b);
-            if (HILO)
-              lo[y] = pack_bf16x2(a - __uint_as_float(hi[y] << 16),
-                                  b - __uint_as_float(hi[y] & 0xFFFF0000u));
-          }
-          if (row >= m) {
-            // behind the sequence: whatever these rows hold (NaN among it) must not reach
-            // the products over tokens, V' and V as factors of 0 no more than K
-            for (int y = 0; y < 4; ++y) hi[y] = lo[y] = 0u;
-            *reinterpret_cast<uint4*>(v + off) = make_uint4(0u, 0u, 0u, 0u);
+        // 16 bytes a step, at the address they have in the swizzled tile: only its row counts
+        uint8_t* v = smem + L::kV + vs * L::kBox + tid * 16;
+        uint8_t* vp = smem + L::kVp + tid * 16;
+        const int row0 = tid / 8;
+        if (m < kChunk) {
+          // Behind the sequence: whatever these rows hold (NaN among it) must not reach the
+          // products over tokens, in which 0 times it would still be NaN.
+          for (int x = 0; x < 8; ++x) {
+            if (row0 + x * 16 < m) continue;
+            *reinterpret_cast<uint4*>(v + x * 2048) = make_uint4(0u, 0u, 0u, 0u);
             for (int y = 0; y < L::kBoxes; ++y)
-              *reinterpret_cast<uint4*>(smem + L::kK + s * L::kTile + y * L::kBox + off) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(smem + L::kK + s * L::kTile + y * L::kBox + tid * 16 +
+                                        x * 2048) = make_uint4(0u, 0u, 0u, 0u);
           }
-          *reinterpret_cast<uint4*>(vp + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          if (HILO)
-            *reinterpret_cast<uint4*>(vp + L::kBox + off) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if (t > 0 && !(ok = mbar_wait_w(u_full, (t - 1) & 1, wctx))) break;
+#pragma unroll 1
+        for (int x0 = 0; x0 < 8; x0 += 2) {
+          uint4 in[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            in[x] = *reinterpret_cast<const uint4*>(v + (x0 + x) * 2048);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int row = row0 + (x0 + x) * 16;
+            const float f = ps.vs * ex2_approx(l2 * static_cast<float>(
+                                                        rev ? row + 1 : max(0, m - 1 - row)));
+            uint32_t hi[4], lo[4];
+            const uint32_t wds[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float2 a = mul2(make_float2(__uint_as_float(wds[y] << 16),
+                                                __uint_as_float(wds[y] & 0xFFFF0000u)),
+                                    make_float2(f, f));
+              hi[y] = pack_bf16x2(a.x, a.y);
+              const float2 b = fma2(make_float2(__uint_as_float(hi[y] << 16),
+                                                __uint_as_float(hi[y] & 0xFFFF0000u)),
+                                    make_float2(-1.0f, -1.0f), a);
+              lo[y] = pack_bf16x2(b.x, b.y);
+            }
+            uint8_t* dst = vp + (x0 + x) * 2048;
+            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + L::kBox) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(vp_full);
-        if (OUT) {
-          if (t > 0 && !(ok = write_out(t - 1))) break;
-          o_row = i < m ? ps.out + it.s.tma_b * ps.o_sb +
-                              (it.s.row0 + c * kChunk + i) * ps.o_sn + it.h * ps.o_sh +
-                              it.slice * kCols
-                        : nullptr;
-          o_f1 = ps.o1 * ex2_approx(l2 * static_cast<float>(rev ? m - 1 - i : i + 1));
-          o_f2 = ps.o2;
-        }
       }
     }
-    if (OUT && ok && t > 0) write_out(t - 1);
+  } else if (warp < kWarpS) {
+    // ---------------------------------------------------------------- the outputs
+    if (OUT) {
+      const int wq = warp & 3, i = wq * 32 + lane;
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+      uint8_t* box = smem + L::kO + wq * 4096;  // 32 rows of 128 swizzled bytes
+      int t = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int w = snake_item(k);
+        if (w >= p.nitems) break;
+        const Item it = decode<D>(p, order, w);
+        const LinPass& ps = p.pass[it.pass];
+        const bool rev = ps.reverse != 0;
+        const float l2 = clamped_decay(p, it.h) * kLog2e;
+        for (int j = 0; j < it.cn; ++j, ++t) {
+          const int c = chunk_of(it, rev, j), m = valid_of(it, c);
+          const float f = ps.o1 * ex2_approx(l2 * static_cast<float>(rev ? m - 1 - i : i + 1));
+          const float2 f1 = make_float2(f, f), f2 = make_float2(ps.o2, ps.o2);
+          if (lane == 0) bulk_wait_read_0();  // the box's last store has read it
+          __syncwarp();
+          if (!(ok = mbar_wait_w(pv_done + t % VS, (t / VS) & 1, wctx))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            uint32_t a[16], b[16], pk[8];
+            tmem_ld16(t_lane + L::kTO1 + x * 16, a);
+            tmem_ld16(t_lane + L::kTO2 + x * 16, b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const float2 o = fma2(
+                  make_float2(__uint_as_float(a[2 * y]), __uint_as_float(a[2 * y + 1])), f1,
+                  mul2(make_float2(__uint_as_float(b[2 * y]), __uint_as_float(b[2 * y + 1])),
+                       f2));
+              pk[y] = i < m ? pack_bf16x2(o.x, o.y) : 0u;
+            }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              *reinterpret_cast<uint4*>(box + lane * 128 + (((2 * x + y) ^ (lane & 7)) << 4)) =
+                  make_uint4(pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
+          }
+          tc_fence_before();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty);
+          const int row = c * kChunk + wq * 32;  // of the sequence
+          if (!p.cu || wq * 32 + 32 <= m) {
+            // padded: rows behind the sequence are 0, rows behind the tensor not written
+            if (lane == 0 && (p.cu || row < p.N)) {
+              tma_store_4d(p.map + ps.o, box, it.slice * kCols, it.s.row0 + row, it.h,
+                           it.s.tma_b);
+              bulk_commit_group();
+            }
+          } else {
+            // packed: the rows behind belong to the next sequence
+            __nv_bfloat16* out = ps.out + (it.s.row0 + row) * ps.o_sn + it.h * ps.o_sh +
+                                 it.slice * kCols;
+            for (int r = lane / 8; r < 32 && wq * 32 + r < m; r += 4)
+              *reinterpret_cast<uint4*>(out + r * ps.o_sn + (lane % 8) * 8) =
+                  *reinterpret_cast<const uint4*>(box + r * 128 + (((lane % 8) ^ (r & 7)) << 4));
+            __syncwarp();
+          }
+        }
+        if (ok && !p.cu) {
+          // Rows behind the last chunk of a padded sequence, within the item's segment, are 0
+          // (those inside it came out of the chunk as 0).
+          const int lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk) + wq * 32;
+          const int hi = it.seg == p.nseg - 1 ? p.N
+                                              : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
+          if (lo < hi) {
+            if (lane == 0) bulk_wait_read_0();
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<uint4*>(box + x * 512 + lane * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              for (int row = lo; row < hi; row += kChunk)
+                tma_store_4d(p.map + ps.o, box, it.slice * kCols, row, it.h, it.s.tma_b);
+              bulk_commit_group();
+            }
+          }
+        }
+      }
+      if (lane == 0) bulk_wait_all();
+      __syncwarp();
+    }
   } else {
     // ---------------------------------------------------------------- the state
-    // d = 128: a thread holds one row of the state, 64 columns; d = 64: half a row, the
-    // second half from the copy of the row in lanes 64-127 of U.
+    // d = 128: a thread holds one row of the state, 64 columns; d = 64: half a row, the second
+    // half from the copy of the row in lanes 64-127 of U.
     constexpr int kHold = D == 128 ? 64 : 32;
     const int wq = warp & 3;
     const int row = D == 128 ? wq * 32 + lane : (wq & 1) * 32 + lane;
@@ -557,8 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t bh = static_cast<int64_t>(it.b) * p.H + it.h;
       float* seg = ps.seg + ((bh * p.nseg + it.seg) * D + row) * D + it.slice * kCols + col0;
       // exp in 64 bits: the factor is applied once a chunk, so its error adds up
-      const double g = static_cast<double>(clamped_decay(p, it.h));
-      const float full = static_cast<float>(exp(g * kChunk));
+      const double g_log = static_cast<double>(clamped_decay(p, it.h));
+      const float full = static_cast<float>(exp(g_log * kChunk));
+      const float part = static_cast<float>(exp(g_log * (it.s.n % kChunk)));  // a last chunk's
       if (OUT && p.nseg > 1) {
         if (it.cn > 0)
 #pragma unroll
@@ -593,20 +715,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(r_full);
         }
-        if (!(ok = mbar_wait_w(u_full + (t & 1), (t >> 1) & 1, wctx))) break;
+        if (!(ok = mbar_wait_w(u_full, t & 1, wctx))) break;
         tc_fence_after();
-        const float f = m == kChunk ? full : static_cast<float>(exp(g * m));
+        const float f = m == kChunk ? full : part;
 #pragma unroll
-        for (int c = 0; c < kHold; c += 32) {
-          uint32_t u[32];
-          tmem_ld32(t_lane + (t & 1) * 64 + c, u);
+        for (int c = 0; c < kHold; c += 8) {
+          uint32_t u[8], e[8];
+          tmem_ld8(t_lane + c, u);
+          tmem_ld8(t_lane + kCols + c, e);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) r[c + x] = fmaf(f, r[c + x], __uint_as_float(u[x]));
+          for (int x = 0; x < 8; ++x)
+            r[c + x] = fmaf(f, r[c + x], __uint_as_float(u[x]) + __uint_as_float(e[x]));
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(u_empty + (t & 1));
+        if (lane == 0) mbar_arrive(u_empty);
       }
       float* dst = !OUT ? (it.cn > 0 ? seg : nullptr)
                    : (p.nseg == 1 && ps.fin)
@@ -741,11 +865,11 @@ void segments(int npass, int B, int N, int H, int d, int* nseg, int* seg_chunks)
   *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
 }
 
-template <int D, bool OUT, bool HILO>
+template <int D, bool OUT>
 int launch_one(const LinParams& p, cudaStream_t stream) {
-  using L = LinLayout<D, HILO>;
+  using L = LinLayout<D>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory");
-  auto kern = linear_kernel<D, OUT, HILO>;
+  auto kern = linear_kernel<D, OUT>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return cuda_status(e);
@@ -755,15 +879,13 @@ int launch_one(const LinParams& p, cudaStream_t stream) {
 
 template <int D>
 int launch(const LinParams& p, cudaStream_t stream) {
-  bool fin = false;
-  for (int i = 0; i < p.npass; ++i) fin = fin || p.pass[i].fin;
-  if (p.nseg == 1)
-    return fin ? launch_one<D, true, true>(p, stream) : launch_one<D, true, false>(p, stream);
-  int rc = fin ? launch_one<D, false, true>(p, stream) : launch_one<D, false, false>(p, stream);
-  if (rc != SIGATTN_OK) return rc;
-  k_linear_join<D><<<dim3(D * D / 1024, p.B * p.H, p.npass), 256, 0, stream>>>(p);
-  if ((rc = cuda_status(cudaGetLastError())) != SIGATTN_OK) return rc;
-  return launch_one<D, true, false>(p, stream);
+  if (p.nseg > 1) {
+    int rc = launch_one<D, false>(p, stream);
+    if (rc != SIGATTN_OK) return rc;
+    k_linear_join<D><<<dim3(D * D / 1024, p.B * p.H, p.npass), 256, 0, stream>>>(p);
+    if ((rc = cuda_status(cudaGetLastError())) != SIGATTN_OK) return rc;
+  }
+  return launch_one<D, true>(p, stream);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -791,7 +913,8 @@ int check_sizes(int B, int N, int64_t T, int H, int d, bool packed) {
 
 // Fills what the passes share; the tensor maps are those of t[0..n).
 int fill(LinParams* p, int npass, int B, int N, int64_t T, int H, int d, const int32_t* lengths,
-         const int32_t* cu, const float* log_decay, const TensorDesc* t, int n) {
+         const int32_t* cu, const float* log_decay, const TensorDesc* t, int n,
+         const TensorDesc* out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
@@ -801,6 +924,16 @@ int fill(LinParams* p, int npass, int B, int N, int64_t T, int H, int d, const i
   if ((rc = status_ptr(&p->status)) != SIGATTN_OK) return rc;
   for (int i = 0; i < n; ++i)
     if ((rc = make_tmap_bf16(&p->map[i], t[i], cu ? 1 : B, H, d)) != SIGATTN_OK) return rc;
+  for (int i = 0; i < npass; ++i) {
+    if ((rc = make_tmap_bf16(&p->map[n + i], out[i], cu ? 1 : B, H, d, 32)) != SIGATTN_OK)
+      return rc;
+    LinPass& ps = p->pass[i];
+    ps.o = n + i;
+    ps.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out[i].ptr));
+    ps.o_sb = out[i].sb;
+    ps.o_sn = out[i].sn;
+    ps.o_sh = out[i].sh;
+  }
   p->npass = npass;
   p->B = B;
   p->H = H;
@@ -813,13 +946,6 @@ int fill(LinParams* p, int npass, int B, int N, int64_t T, int H, int d, const i
   p->log_decay = log_decay;
   p->wait_ns = wait_limit_ns();
   return SIGATTN_OK;
-}
-
-void set_out(LinPass* ps, const TensorDesc& o) {
-  ps->out = static_cast<__nv_bfloat16*>(const_cast<void*>(o.ptr));
-  ps->o_sb = o.sb;
-  ps->o_sn = o.sn;
-  ps->o_sh = o.sh;
 }
 
 size_t workspace_bytes_of(int npass, int B, int N, int H, int d) {
@@ -865,13 +991,13 @@ extern "C" int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const i
     return SIGATTN_ERR_ALIGNMENT;
   LinParams p;
   std::memset(&p, 0, sizeof(p));
-  if ((rc = fill(&p, 1, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 3)) != SIGATTN_OK)
+  if ((rc = fill(&p, 1, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 3, &to)) !=
+      SIGATTN_OK)
     return rc;
   LinPass& ps = p.pass[0];
   ps.q = 0, ps.k = 1, ps.v = 2;
   ps.o1 = ps.o2 = scale;
   ps.vs = 1.0f;
-  set_out(&ps, to);
   ps.init = state;
   ps.init_sr = d;
   ps.init_sc = 1;
@@ -896,21 +1022,22 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
   if (rc != SIGATTN_OK) return rc;
   if (!log_decay || !std::isfinite(scale) || (packed && lengths)) return SIGATTN_ERR_INVALID;
   const int rows = packed ? static_cast<int>(T) : N;
-  TensorDesc t[4], tdq, tdk, tdv;
+  TensorDesc t[4], out[3];
   if ((rc = check_tensor(q, q_strides, rows, &t[0])) != SIGATTN_OK) return rc;
   if ((rc = check_tensor(k, k_strides, rows, &t[1])) != SIGATTN_OK) return rc;
   if ((rc = check_tensor(v, v_strides, rows, &t[2])) != SIGATTN_OK) return rc;
   if ((rc = check_tensor(dout, do_strides, rows, &t[3])) != SIGATTN_OK) return rc;
-  if ((rc = check_tensor(dq, dq_strides, rows, &tdq)) != SIGATTN_OK) return rc;
-  if ((rc = check_tensor(dk, dk_strides, rows, &tdk)) != SIGATTN_OK) return rc;
-  if ((rc = check_tensor(dv, dv_strides, rows, &tdv)) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dq, dq_strides, rows, &out[0])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dk, dk_strides, rows, &out[1])) != SIGATTN_OK) return rc;
+  if ((rc = check_tensor(dv, dv_strides, rows, &out[2])) != SIGATTN_OK) return rc;
   const size_t need = workspace_bytes_of(3, B, N, H, d);
   if (need && (!workspace || workspace_bytes < need)) return SIGATTN_ERR_INVALID;
   if (!aligned16(state) || !aligned16(dfinal_state) || !aligned16(dstate) || !aligned16(workspace))
     return SIGATTN_ERR_ALIGNMENT;
   LinParams p;
   std::memset(&p, 0, sizeof(p));
-  if ((rc = fill(&p, 3, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 4)) != SIGATTN_OK)
+  if ((rc = fill(&p, 3, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 4, out)) !=
+      SIGATTN_OK)
     return rc;
   const size_t part = need / 3 / sizeof(float);
   for (int i = 0; i < 3; ++i)
@@ -920,7 +1047,6 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
   a.q = 3, a.k = 2, a.v = 1;
   a.o1 = a.o2 = scale;
   a.vs = 1.0f;
-  set_out(&a, tdq);
   a.init = state;
   a.init_sr = 1;
   a.init_sc = d;
@@ -930,7 +1056,6 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
   b.reverse = 1;
   b.o1 = 1.0f;
   b.o2 = b.vs = scale;
-  set_out(&b, tdk);
   b.init = dfinal_state;
   b.init_sr = 1;
   b.init_sc = d;
@@ -940,7 +1065,6 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
   c.reverse = 1;
   c.o1 = 1.0f;
   c.o2 = c.vs = scale;
-  set_out(&c, tdv);
   c.init = dfinal_state;
   c.init_sr = d;
   c.init_sc = 1;
