@@ -34,10 +34,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kChunk = 128;
 constexpr int kCols = 64;       // value columns of a work item
 constexpr int kSms = 148;       // B200
-constexpr int kMaxSorted = 512;  // batches up to this size are walked longest-first
-constexpr int kThreads = 576;
-// first warps of P, V', the outputs and the state, four each
-constexpr int kWarpP = 2, kWarpV = 6, kWarpO = 10, kWarpS = 14;
+constexpr int kMaxSorted = 256;  // batches up to this size are walked longest-first
+constexpr int kRing = 8;         // work items decoded ahead
+constexpr int kThreads = 736;
+// first warps of P (4), V' (4), the outputs (4) and the state (8); last, the items' (1)
+constexpr int kWarpP = 2, kWarpV = 6, kWarpO = 10, kWarpS = 14, kWarpI = 22;
 
 struct LinPass {
   int q, k, v;     // which of the tensor maps stand in the places of q, k, v
@@ -91,16 +92,20 @@ __device__ __forceinline__ Seq sequence(const LinParams& p, int b) {
   return s;
 }
 
-struct Item {
-  int b, h, slice, pass, seg;
+struct alignas(16) Item {
   Seq s;
-  int c0, cn;  // its chunks [c0, c0 + cn)
+  int pass;     // -1: no more items
+  int b, h, slice, seg;
+  int c0, cn;   // its chunks [c0, c0 + cn)
+  float l2;     // log2 lambda
+  float full;   // lambda^128, and lambda^m for the last chunk of the sequence.  exp in 64 bits:
+  float part;   // the state is multiplied by them once a chunk, so their errors add up
 };
 
 // Work item w: sequences longest-first (order), then segment, head, pass and slice of value
 // columns, so that the items that read the same rows run side by side.
 template <int D>
-__device__ __forceinline__ Item decode(const LinParams& p, const uint16_t* order, int w) {
+__device__ __forceinline__ Item decode(const LinParams& p, const uint8_t* order, int w) {
   Item it;
   it.slice = w % (D / kCols);
   w /= D / kCols;
@@ -141,12 +146,13 @@ struct LinLayout {
   static constexpr int kO = kR + D * 128;           // outputs on their way, 4 KB per warp
   static constexpr int kBar = kO + kBox;
   // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2] u_full u_empty
-  // vp_full r_full o_empty done
-  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 10;
+  // vp_full r_full o_empty done item_full[8] item_empty[8]
+  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 10 + 2 * kRing;
   static constexpr int kMisc = kBar + 8 * kNumBars;  // tmem base, abort, drain flags
   static constexpr int kPow = kMisc + 16;            // powers of lambda, 32 per warp of P
-  static constexpr int kOrder = kPow + 4 * 32 * 4;
-  static constexpr int kBytes = kOrder + 2 * kMaxSorted;
+  static constexpr int kItems = kPow + 4 * 32 * 4;   // work items decoded ahead
+  static constexpr int kOrder = kItems + kRing * sizeof(Item);
+  static constexpr int kBytes = kOrder + kMaxSorted;
   static constexpr int kAlloc = kBytes + 1024;       // slack for 1024-byte alignment
   // TMEM columns
   static constexpr int kTS = 0;     // two S / P buffers of 128
@@ -204,44 +210,46 @@ __device__ __forceinline__ void mma_kv_commit_w(uint32_t d_tmem, uint32_t a_lo, 
 #undef SIGATTN_LIN_HEAD
 #undef SIGATTN_LIN_TAIL
 
-// 16 columns from c0 of row i of S, weighted by lambda^|i - j|, masked and rounded.  pow: the
-// powers of lambda over 32 columns, see the caller.
-__device__ __forceinline__ void weigh(const uint32_t (&s)[16], int c0, int m, bool rev, int i,
-                                      float l2, const float* pow, uint32_t (&pk)[8]) {
-  const int at = c0 - i;      // j - i of the first column
-  const int last = m - c0;    // columns from here on are behind the sequence
-  if (c0 / 32 != i / 32) {
-    const int blk = c0 & ~31;
-    const float f = ex2_approx(l2 * static_cast<float>(rev ? blk - i : i - blk - 31));
-    const float2 f2 = make_float2(f, f);
-    float v[16];
+// lambda^|i - j| in blocks of 32 columns: off the diagonal the product of a row's power f up
+// to the block's near end and a column's power pow[c] from there, both at most 1 for any
+// decay; in the diagonal block, where that split would overflow, exp2 of each element.
+
+// 32 columns of a row of S off the diagonal.  Columns from `last` on are behind the sequence.
+__device__ __forceinline__ void weigh_far(const uint32_t (&s)[32], float f, const float* pow,
+                                          int last, uint32_t (&pk)[16]) {
+  const float2 f2 = make_float2(f, f);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(s[c]);
-    if (rev && last < 16) {
+  for (int c = 0; c < 32; c += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(pow + c);
+    const float2 a = mul2(mul2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), f2),
+                          make_float2(q.x, q.y));
+    const float2 b =
+        mul2(mul2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), f2),
+             make_float2(q.z, q.w));
+    pk[c / 2] = pack_bf16x2(a.x, a.y);
+    pk[c / 2 + 1] = pack_bf16x2(b.x, b.y);
+  }
+  if (last < 32) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) v[c] = c < last ? v[c] : 0.0f;
+    for (int c = 0; c < 16; ++c)
+      pk[c] &= (2 * c < last ? 0xFFFFu : 0u) | (2 * c + 1 < last ? 0xFFFF0000u : 0u);
+  }
+}
+
+// 16 columns of row i of S in the diagonal block; at = j - i of the first.
+__device__ __forceinline__ void weigh_near(const uint32_t (&s)[16], float l2, bool rev, int at,
+                                           int last, uint32_t (&pk)[8]) {
+  const float x0 = l2 * static_cast<float>(rev ? at : -at), dx = rev ? l2 : -l2;
+#pragma unroll
+  for (int c = 0; c < 16; c += 2) {
+    float f[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const bool keep = rev ? at + c + y >= 0 && c + y < last : at + c + y <= 0;
+      const float x = ex2_approx(fmaf(dx, static_cast<float>(c + y), x0));
+      f[y] = keep ? __uint_as_float(s[c + y]) * x : 0.0f;
     }
-#pragma unroll
-    for (int c = 0; c < 16; c += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(pow + (c0 & 16) + c);
-      const float2 a = mul2(mul2(make_float2(v[c], v[c + 1]), f2), make_float2(q.x, q.y));
-      const float2 b = mul2(mul2(make_float2(v[c + 2], v[c + 3]), f2), make_float2(q.z, q.w));
-      pk[c / 2] = pack_bf16x2(a.x, a.y);
-      pk[c / 2 + 1] = pack_bf16x2(b.x, b.y);
-    }
-  } else {
-    const float x0 = l2 * static_cast<float>(rev ? at : -at), dx = rev ? l2 : -l2;
-#pragma unroll
-    for (int c = 0; c < 16; c += 2) {
-      float f[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const bool keep = rev ? at + c + y >= 0 && c + y < last : at + c + y <= 0;
-        const float x = ex2_approx(fmaf(dx, static_cast<float>(c + y), x0));
-        f[y] = keep ? __uint_as_float(s[c + y]) * x : 0.0f;
-      }
-      pk[c / 2] = pack_bf16x2(f[0], f[1]);
-    }
+    pk[c / 2] = pack_bf16x2(f[0], f[1]);
   }
 }
 
@@ -278,10 +286,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* r_full = vp_full + 1;
   uint64_t* o_empty = r_full + 1;
   uint64_t* done = o_empty + 1;
+  uint64_t* item_full = done + 1;
+  uint64_t* item_empty = item_full + kRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
-  uint16_t* order = reinterpret_cast<uint16_t*>(smem + L::kOrder);
+  Item* items = reinterpret_cast<Item*>(smem + L::kItems);
+  uint8_t* order = smem + L::kOrder;
   const WaitCtx wctx{p.status, p.wait_ns, abort_flag};
 
   if (threadIdx.x == 0) {
@@ -298,11 +309,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p_full + i, 4);
     }
     mbar_init(u_full, 1);
-    mbar_init(u_empty, 4);
+    mbar_init(u_empty, 8);
     mbar_init(vp_full, 4);
-    mbar_init(r_full, 4);
+    mbar_init(r_full, 8);
     mbar_init(o_empty, 4);
     mbar_init(done, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(item_full + i, 1);
+      mbar_init(item_empty + i, OUT ? 21 : 13);  // the warps that take items
+    }
     *abort_flag = 0;
     *drain_flag = 0;
     fence_barrier_init();
@@ -317,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
       int rank = 0;
       for (int x = 0; x < p.B; ++x) rank += len[x] > len[b] || (len[x] == len[b] && x < b);
-      order[rank] = static_cast<uint16_t>(b);
+      order[rank] = static_cast<uint8_t>(b);
     }
     // the copies that overwrite len go through the async proxy
     fence_proxy_async_smem();
@@ -326,16 +341,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // The k-th work item of this CTA, from the ring; false at the end of the list (and after a
+  // wait that gave up).  Called by whole warps; every one of them takes every item.
+  auto take = [&](int k, Item& it) -> bool {
+    if (!mbar_wait_w(item_full + k % kRing, (k / kRing) & 1, wctx)) return false;
+    it = items[k % kRing];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(item_empty + k % kRing);
+    return it.pass >= 0;
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int t = 0, tv = 0;  // chunks whose Q and K, whose V copies are issued
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int w = snake_item(k);
-        if (w >= p.nitems) break;
-        const Item it = decode<D>(p, order, w);
+    int t = 0, tv = 0;  // chunks whose Q and K, whose V copies are issued
+    bool ok = true;
+    Item it;
+    for (int k = 0; ok && take(k, it); ++k) {
+      if (lane == 0) {
         const LinPass& ps = p.pass[it.pass];
         const CUtensorMap* mq = p.map + ps.q;
         const CUtensorMap* mk = p.map + ps.k;
@@ -360,6 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++tv;
         }
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+    if (lane == 0) {
       if (*abort_flag) {
         // Let the copies still in flight land before the CTA's shared memory goes away.
         const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
@@ -377,11 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, kCols, true);
     constexpr uint32_t idesc_u = idesc_bf16_f32(128, 2 * kCols, true, true);
     int total = 0;
-    for (int k = 0;; ++k) {
-      const int w = snake_item(k);
-      if (w >= p.nitems) break;
-      total += decode<D>(p, order, w).cn;
-    }
+    for (int k = lane; snake_item(k) < p.nitems; k += 32)
+      total += decode<D>(p, order, snake_item(k)).cn;
+    total = __reduce_add_sync(0xFFFFFFFFu, total);
     auto ready = [](uint64_t* bar, int phase) {
       return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)) != 0;
     };
@@ -453,21 +476,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait_w(done, 0, drain);
   } else if (warp < kWarpV) {
     // ---------------------------------------------------------------- P = decayed, masked S
-    // lambda^|i - j| in blocks of 32 columns: off the diagonal the product of a row's power up
-    // to the block's near end and a column's power from there, both at most 1 for any decay;
-    // in the diagonal block, where that split would overflow, exp2 of each element.
     if (OUT) {
       const int wq = warp & 3, i = wq * 32 + lane;
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
       float* pow = reinterpret_cast<float*>(smem + L::kPow) + wq * 32;
       int t = 0;
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int w = snake_item(k);
-        if (w >= p.nitems) break;
-        const Item it = decode<D>(p, order, w);
+      Item it;
+      for (int k = 0; ok && take(k, it); ++k) {
         const bool rev = p.pass[it.pass].reverse != 0;
-        const float l2 = clamped_decay(p, it.h) * kLog2e;
+        const float l2 = it.l2;
         __syncwarp();
         pow[lane] = ex2_approx(l2 * static_cast<float>(rev ? lane : 31 - lane));
         __syncwarp();
@@ -476,23 +494,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sb = t_lane + L::kTS + (t & 1) * 128;
           if (!(ok = mbar_wait_w(s_full + (t & 1), (t >> 1) & 1, wctx))) break;
           tc_fence_after();
-          uint32_t pk[8];
-          // Columns [first, end) have kept elements, 16 at a time; P of keys c0.. goes to
-          // column (c0 / 64) 64 + (c0 % 64) / 2, where S has been read by then.
-          const int first = rev ? wq * 32 : 0, end = rev ? 128 : wq * 32 + 32;
+          // P of keys c0.. goes to column (c0 / 64) 64 + (c0 % 64) / 2, where S has been read
+          // by then.
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 16) {
-            const uint32_t dst = sb + (c0 & 64) + (c0 & 63) / 2;
-            if (c0 < first || c0 >= end) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) pk[c] = 0u;
+          for (int blk = 0; blk < 4; ++blk) {
+            const uint32_t src = sb + blk * 32, dst = sb + (blk & 2) * 32 + (blk & 1) * 16;
+            const int last = m - blk * 32;
+            if (blk == wq) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < 32; c0 += 16) {
+                uint32_t sr[16], pk[8];
+                tmem_ld16(src + c0, sr);
+                tmem_wait_ld();
+                weigh_near(sr, l2, rev, c0 - lane, last - c0, pk);
+                tmem_st8(dst + c0 / 2, pk);
+              }
             } else {
-              uint32_t sr[16];
-              tmem_ld16(sb + c0, sr);
-              tmem_wait_ld();
-              weigh(sr, c0, m, rev, i, l2, pow, pk);
+              uint32_t pk[16];
+              if (rev ? blk < wq : blk > wq) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) pk[c] = 0u;
+              } else {
+                uint32_t sr[32];
+                tmem_ld32(src, sr);
+                tmem_wait_ld();
+                const float f = ex2_approx(
+                    l2 * static_cast<float>(rev ? blk * 32 - i : i - blk * 32 - 31));
+                weigh_far(sr, f, pow, last, pk);
+              }
+              tmem_st16(dst, pk);
             }
-            tmem_st8(dst, pk);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -506,13 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - kWarpV * 32;
     int t = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const int w = snake_item(k);
-      if (w >= p.nitems) break;
-      const Item it = decode<D>(p, order, w);
+    Item it;
+    for (int k = 0; ok && take(k, it); ++k) {
       const LinPass& ps = p.pass[it.pass];
       const bool rev = ps.reverse != 0;
-      const float l2 = clamped_decay(p, it.h) * kLog2e;
+      const float l2 = it.l2;
       for (int j = 0; j < it.cn; ++j, ++t) {
         const int m = valid_of(it, chunk_of(it, rev, j));
         const int vs = t % VS, s = t % ST;
@@ -576,13 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* box = smem + L::kO + wq * 4096;  // 32 rows of 128 swizzled bytes
       int t = 0;
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const int w = snake_item(k);
-        if (w >= p.nitems) break;
-        const Item it = decode<D>(p, order, w);
+      Item it;
+      for (int k = 0; ok && take(k, it); ++k) {
         const LinPass& ps = p.pass[it.pass];
         const bool rev = ps.reverse != 0;
-        const float l2 = clamped_decay(p, it.h) * kLog2e;
+        const float l2 = it.l2;
         for (int j = 0; j < it.cn; ++j, ++t) {
           const int c = chunk_of(it, rev, j), m = valid_of(it, c);
           const float f = ps.o1 * ex2_approx(l2 * static_cast<float>(rev ? m - 1 - i : i + 1));
@@ -657,30 +684,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) bulk_wait_all();
       __syncwarp();
     }
-  } else {
+  } else if (warp < kWarpI) {
     // ---------------------------------------------------------------- the state
-    // d = 128: a thread holds one row of the state, 64 columns; d = 64: half a row, the second
-    // half from the copy of the row in lanes 64-127 of U.
-    constexpr int kHold = D == 128 ? 64 : 32;
-    const int wq = warp & 3;
+    // Eight warps: d = 128, a thread holds 32 columns of one row; d = 64, 16 columns, half of
+    // the warps reading the copy of the rows in lanes 64-127 of U.
+    constexpr int kHold = D == 128 ? 32 : 16;
+    const int wq = warp & 3, g = (warp - kWarpS) / 4;
     const int row = D == 128 ? wq * 32 + lane : (wq & 1) * 32 + lane;
-    const int col0 = D == 128 ? 0 : (wq >> 1) * 32;
+    const int col0 = D == 128 ? g * 32 : g * 32 + (wq >> 1) * 16;
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16) + L::kTU + col0;
     float r[kHold];
     int t = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const int w = snake_item(k);
-      if (w >= p.nitems) break;
-      const Item it = decode<D>(p, order, w);
+    Item it;
+    for (int k = 0; ok && take(k, it); ++k) {
       const LinPass& ps = p.pass[it.pass];
       const bool rev = ps.reverse != 0;
       const int64_t bh = static_cast<int64_t>(it.b) * p.H + it.h;
       float* seg = ps.seg + ((bh * p.nseg + it.seg) * D + row) * D + it.slice * kCols + col0;
-      // exp in 64 bits: the factor is applied once a chunk, so its error adds up
-      const double g_log = static_cast<double>(clamped_decay(p, it.h));
-      const float full = static_cast<float>(exp(g_log * kChunk));
-      const float part = static_cast<float>(exp(g_log * (it.s.n % kChunk)));  // a last chunk's
       if (OUT && p.nseg > 1) {
         if (it.cn > 0)
 #pragma unroll
@@ -717,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = mbar_wait_w(u_full, t & 1, wctx))) break;
         tc_fence_after();
-        const float f = m == kChunk ? full : part;
+        const float f = m == kChunk ? it.full : it.part;
 #pragma unroll
         for (int c = 0; c < kHold; c += 8) {
           uint32_t u[8], e[8];
@@ -740,6 +761,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kHold; c += 4)
           *reinterpret_cast<float4*>(dst + c) = make_float4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- the work items
+    // 32 at a time, one per lane, and into the ring as its places get free.
+    bool more = true;
+    for (int k0 = 0; more; k0 += 32) {
+      const int w = snake_item(k0 + lane);
+      Item it{};
+      it.pass = -1;
+      if (w < p.nitems) {
+        it = decode<D>(p, order, w);
+        const float g = clamped_decay(p, it.h);
+        it.l2 = g * kLog2e;
+        it.full = static_cast<float>(exp(static_cast<double>(g) * kChunk));
+        it.part = static_cast<float>(exp(static_cast<double>(g) * (it.s.n % kChunk)));
+      }
+      for (int u = 0; u < 32 && more; ++u) {
+        const int k = k0 + u;
+        bool go = true;
+        if (lane == u) {
+          if (k >= kRing) go = mbar_wait(item_empty + k % kRing, (k / kRing - 1) & 1, wctx);
+          if (go) {
+            items[k % kRing] = it;
+            mbar_arrive(item_full + k % kRing);
+          }
+          go = go && it.pass >= 0;
+        }
+        more = __all_sync(0xFFFFFFFFu, go);
       }
     }
   }
