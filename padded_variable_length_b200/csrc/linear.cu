@@ -36,6 +36,7 @@ constexpr int kCols = 64;       // value columns of a work item
 constexpr int kSms = 148;       // B200
 constexpr int kMaxSorted = 256;  // batches up to this size are walked longest-first
 constexpr int kRing = 8;         // work items decoded ahead
+constexpr int kMaxSegs = 16;     // of a sequence
 constexpr int kThreads = 736;
 // first warps of P (4), V' (4), the outputs (4) and the state (8); last, the items' (1)
 constexpr int kWarpP = 2, kWarpV = 6, kWarpO = 10, kWarpS = 14, kWarpI = 22;
@@ -131,24 +132,27 @@ __device__ __forceinline__ int valid_of(const Item& it, int c) {
   return min(kChunk, it.s.n - c * kChunk);
 }
 
-template <int D>
+template <int D, bool OUT>
 struct LinLayout {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBox = 128 * 128;            // 128 tokens x 64 bf16
   static constexpr int kTile = kBoxes * kBox;       // a Q or K tile
-  static constexpr int kSt = D == 64 ? 3 : 2;       // stages of Q and K
-  static constexpr int kVs = D == 64 ? 4 : 2;       // stages of V
-  static constexpr int kQ = 0;
-  static constexpr int kK = kQ + kSt * kTile;
-  static constexpr int kV = kK + kSt * kTile;
+  // Stages of Q and K, and of V.  Without the outputs there are no Q, R and O, and their room
+  // goes to stages and a second V'.
+  static constexpr int kSt = OUT ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
+  static constexpr int kVs = OUT ? (D == 64 ? 4 : 2) : (D == 64 ? 4 : 3);
+  static constexpr int kNu = OUT ? 1 : 2;           // buffers of V' and U
+  static constexpr int kK = 0;
+  static constexpr int kQ = kK + kSt * kTile;
+  static constexpr int kV = kQ + (OUT ? kSt * kTile : 0);
   static constexpr int kVp = kV + kVs * kBox;       // V' and, behind it, its rounding error
-  static constexpr int kR = kVp + 2 * kBox;         // bf16 state, D rows of 64
-  static constexpr int kO = kR + D * 128;           // outputs on their way, 4 KB per warp
-  static constexpr int kBar = kO + kBox;
-  // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2] u_full u_empty
-  // vp_full r_full o_empty done item_full[8] item_empty[8]
-  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 10 + 2 * kRing;
-  static constexpr int kMisc = kBar + 8 * kNumBars;  // tmem base, abort, drain flags
+  static constexpr int kR = kVp + kNu * 2 * kBox;   // bf16 state, D rows of 64
+  static constexpr int kO = kR + (OUT ? D * 128 : 0);  // outputs on their way, 4 KB per warp
+  static constexpr int kBar = kO + (OUT ? kBox : 0);
+  // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2]
+  // u_full[2] u_empty[2] vp_full[2] r_full o_empty done item_full[8] item_empty[8]
+  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 13 + 2 * kRing;
+  static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;  // tmem base, flags
   static constexpr int kPow = kMisc + 16;            // powers of lambda, 32 per warp of P
   static constexpr int kItems = kPow + 4 * 32 * 4;   // work items decoded ahead
   static constexpr int kOrder = kItems + kRing * sizeof(Item);
@@ -267,8 +271,9 @@ __device__ __forceinline__ void weigh_near(const uint32_t (&s)[16], float l2, bo
 template <int D, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinParams p) {
-  using L = LinLayout<D>;
+  using L = LinLayout<D, OUT>;
   constexpr int ST = L::kSt, VS = L::kVs;
+  constexpr int NU = L::kNu;
   extern __shared__ uint8_t smem_raw[];
   // (an offset, not a cast of the rounded address, which would lose its address space)
   uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
@@ -281,9 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = pv_done + VS;
   uint64_t* p_full = s_full + 2;
   uint64_t* u_full = p_full + 2;       // K^T V' complete: U ready, V' free
-  uint64_t* u_empty = u_full + 1;
-  uint64_t* vp_full = u_empty + 1;
-  uint64_t* r_full = vp_full + 1;
+  uint64_t* u_empty = u_full + 2;
+  uint64_t* vp_full = u_empty + 2;
+  uint64_t* r_full = vp_full + 2;
   uint64_t* o_empty = r_full + 1;
   uint64_t* done = o_empty + 1;
   uint64_t* item_full = done + 1;
@@ -307,16 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
       mbar_init(p_full + i, 4);
+      mbar_init(u_full + i, 1);
+      mbar_init(u_empty + i, 8);
+      mbar_init(vp_full + i, 4);
     }
-    mbar_init(u_full, 1);
-    mbar_init(u_empty, 8);
-    mbar_init(vp_full, 4);
     mbar_init(r_full, 8);
     mbar_init(o_empty, 4);
     mbar_init(done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, OUT ? 21 : 13);  // the warps that take items
+      mbar_init(item_empty + i, OUT ? 21 : 17);  // the warps that take items
     }
     *abort_flag = 0;
     *drain_flag = 0;
@@ -433,15 +438,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++to;
         progress = true;
       }
-      if (tu < (OUT ? ts : total) && ready(vp_full, tu) && (tu == 0 || ready(u_empty, tu - 1)) &&
+      if (tu < (OUT ? ts : total) && ready(vp_full + tu % NU, tu / NU) &&
+          (tu < NU || ready(u_empty + tu % NU, tu / NU - 1)) &&
           (OUT || ready(qk_full + tu % ST, tu / ST))) {
         // U = K^T (V' | its rounding error).  A holds the K columns as rows: 128 for d = 128;
         // for d = 64 the chunk stride of 0 gives them twice, lanes 64-127 a copy of 0-63.
         tc_fence_after();
         const uint32_t k_base = smem_u32(smem + L::kK + (tu % ST) * L::kTile);
-        const uint32_t v_base = smem_u32(smem + L::kVp);
-        mma_kv_commit_w(tmem + L::kTU, sw128_desc_lo(k_base, D == 128 ? L::kBox : 0),
-                        sw128_desc_lo(v_base, L::kBox), kHi, idesc_u, u_full);
+        const uint32_t v_base = smem_u32(smem + L::kVp + tu % NU * 2 * L::kBox);
+        mma_kv_commit_w(tmem + (tu % NU == 0 ? L::kTU : L::kTS), sw128_desc_lo(k_base, D == 128 ? L::kBox : 0),
+                        sw128_desc_lo(v_base, L::kBox), kHi, idesc_u,
+                        u_full + tu % NU);
         if (!OUT) {
           mma_commit_w(qk_empty + tu % ST);
           mma_commit_w(pv_done + tu % VS);
@@ -532,9 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp < kWarpO) {
+  } else if (warp < (OUT ? kWarpO : kWarpS)) {
     // ---------------------------------------------------------------- V'
-    const int tid = threadIdx.x - kWarpV * 32;
+    // (without the outputs their warps take every other chunk)
+    const int tid = (threadIdx.x - kWarpV * 32) % 128, odd = warp >= kWarpO;
     int t = 0;
     bool ok = true;
     Item it;
@@ -544,12 +552,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float l2 = it.l2;
       for (int j = 0; j < it.cn; ++j, ++t) {
         const int m = valid_of(it, chunk_of(it, rev, j));
+        if (!OUT && t % 2 != odd) continue;
         const int vs = t % VS, s = t % ST;
         if (!(ok = mbar_wait_w(v_full + vs, (t / VS) & 1, wctx))) break;
         if (m < kChunk && !(ok = mbar_wait_w(qk_full + s, (t / ST) & 1, wctx))) break;
         // 16 bytes a step, at the address they have in the swizzled tile: only its row counts
         uint8_t* v = smem + L::kV + vs * L::kBox + tid * 16;
-        uint8_t* vp = smem + L::kVp + tid * 16;
+        uint8_t* vp = smem + L::kVp + t % NU * 2 * L::kBox + tid * 16;
         const int row0 = tid / 8;
         if (m < kChunk) {
           // Behind the sequence: whatever these rows hold (NaN among it) must not reach the
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         x * 2048) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        if (t > 0 && !(ok = mbar_wait_w(u_full, (t - 1) & 1, wctx))) break;
+        if (t >= NU && !(ok = mbar_wait_w(u_full + t % NU, (t / NU - 1) & 1, wctx))) break;
 #pragma unroll 1
         for (int x0 = 0; x0 < 8; x0 += 2) {
           uint4 in[2];
@@ -594,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(vp_full);
+        if (lane == 0) mbar_arrive(vp_full + t % NU);
       }
     }
   } else if (warp < kWarpS) {
@@ -692,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp & 3, g = (warp - kWarpS) / 4;
     const int row = D == 128 ? wq * 32 + lane : (wq & 1) * 32 + lane;
     const int col0 = D == 128 ? g * 32 : g * 32 + (wq >> 1) * 16;
-    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16) + L::kTU + col0;
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16) + col0;
     float r[kHold];
     int t = 0;
     bool ok = true;
@@ -736,14 +745,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(r_full);
         }
-        if (!(ok = mbar_wait_w(u_full, t & 1, wctx))) break;
+        if (!(ok = mbar_wait_w(u_full + t % NU, (t / NU) & 1, wctx))) break;
         tc_fence_after();
         const float f = m == kChunk ? it.full : it.part;
+        const int at = t % NU == 0 ? L::kTU : L::kTS;
 #pragma unroll
         for (int c = 0; c < kHold; c += 8) {
           uint32_t u[8], e[8];
-          tmem_ld8(t_lane + c, u);
-          tmem_ld8(t_lane + kCols + c, e);
+          tmem_ld8(t_lane + at + c, u);
+          tmem_ld8(t_lane + at + kCols + c, e);
           tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 8; ++x)
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(u_empty);
+        if (lane == 0) mbar_arrive(u_empty + t % NU);
       }
       float* dst = !OUT ? (it.cn > 0 ? seg : nullptr)
                    : (p.nseg == 1 && ps.fin)
@@ -802,32 +812,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The states that the segments start from, in place of what each leaves from a zero start,
-// and the final state.  One thread per state element and (b, h, pass); four columns each.
+// The states that the segments start from, in place of what each leaves from a zero start, and
+// the final state.  Four state columns per thread; all of a thread's reads are issued before
+// the first is used.
 template <int D>
-__global__ void __launch_bounds__(256) k_linear_join(const __grid_constant__ LinParams p) {
-  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
+__global__ void __launch_bounds__(128) k_linear_join(const __grid_constant__ LinParams p) {
+  __shared__ float factor[2];  // lambda to the tokens of a whole segment, of the last one
+  const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
   const int bh = blockIdx.y, b = bh / p.H, h = bh % p.H;
   const LinPass& ps = p.pass[blockIdx.z];
   const int n = sequence(p, b).n, rows = p.seg_chunks * kChunk;
   const int segs = (n + rows - 1) / rows;
-  const double g = static_cast<double>(clamped_decay(p, h));
-  const float full = static_cast<float>(exp(g * rows));
-  const float part = static_cast<float>(exp(g * (n - (segs - 1) * rows)));  // the last segment
+  float* seg = ps.seg + static_cast<int64_t>(bh) * p.nseg * D * D + e;
+  const auto at = [&](int x) {
+    const int s = ps.reverse ? segs - 1 - x : x;
+    return reinterpret_cast<float4*>(seg + static_cast<int64_t>(s) * D * D);
+  };
+  float4 u[kMaxSegs];
+#pragma unroll
+  for (int x = 0; x < kMaxSegs; ++x)
+    if (x < segs) u[x] = *at(x);
   float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (ps.init) {
-    const float* at = ps.init + static_cast<int64_t>(bh) * D * D + (e / D) * ps.init_sr +
-                      (e % D) * ps.init_sc;
-    r = make_float4(at[0], at[ps.init_sc], at[2 * ps.init_sc], at[3 * ps.init_sc]);
+    const float* from = ps.init + static_cast<int64_t>(bh) * D * D + (e / D) * ps.init_sr +
+                        (e % D) * ps.init_sc;
+    r = make_float4(from[0], from[ps.init_sc], from[2 * ps.init_sc], from[3 * ps.init_sc]);
   }
-  float* seg = ps.seg + static_cast<int64_t>(bh) * p.nseg * D * D + e;
-  for (int x = 0; x < segs; ++x) {
-    const int s = ps.reverse ? segs - 1 - x : x;
-    float4* at = reinterpret_cast<float4*>(seg + static_cast<int64_t>(s) * D * D);
-    const float4 u = *at;
-    *at = r;
-    const float f = s == segs - 1 ? part : full;
-    r = make_float4(fmaf(f, r.x, u.x), fmaf(f, r.y, u.y), fmaf(f, r.z, u.z), fmaf(f, r.w, u.w));
+  if (threadIdx.x < 2)
+    factor[threadIdx.x] = static_cast<float>(
+        exp(static_cast<double>(clamped_decay(p, h)) *
+            (threadIdx.x == 0 ? rows : n - (segs - 1) * rows)));
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < kMaxSegs; ++x) {
+    if (x >= segs) break;
+    *at(x) = r;
+    const float f = factor[x == (ps.reverse ? 0 : segs - 1)];
+    r = make_float4(fmaf(f, r.x, u[x].x), fmaf(f, r.y, u[x].y), fmaf(f, r.z, u[x].z),
+                    fmaf(f, r.w, u[x].w));
   }
   if (ps.fin) *reinterpret_cast<float4*>(ps.fin + static_cast<int64_t>(bh) * D * D + e) = r;
 }
@@ -910,14 +932,14 @@ void segments(int npass, int B, int N, int H, int d, int* nseg, int* seg_chunks)
   const int64_t items = static_cast<int64_t>(npass) * B * H * (d / kCols);
   const int chunks = (N + kChunk - 1) / kChunk;
   int want = items >= kSms ? 1 : static_cast<int>(kSms / items);
-  want = std::max(1, std::min(want, chunks / 4));
+  want = std::max(1, std::min({want, chunks / 4, kMaxSegs}));
   *seg_chunks = (chunks + want - 1) / want;
   *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
 }
 
 template <int D, bool OUT>
 int launch_one(const LinParams& p, cudaStream_t stream) {
-  using L = LinLayout<D>;
+  using L = LinLayout<D, OUT>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory");
   auto kern = linear_kernel<D, OUT>;
   const cudaError_t e =
@@ -932,7 +954,7 @@ int launch(const LinParams& p, cudaStream_t stream) {
   if (p.nseg > 1) {
     int rc = launch_one<D, false>(p, stream);
     if (rc != SIGATTN_OK) return rc;
-    k_linear_join<D><<<dim3(D * D / 1024, p.B * p.H, p.npass), 256, 0, stream>>>(p);
+    k_linear_join<D><<<dim3(D * D / 512, p.B * p.H, p.npass), 128, 0, stream>>>(p);
     if ((rc = cuda_status(cudaGetLastError())) != SIGATTN_OK) return rc;
   }
   return launch_one<D, true>(p, stream);
