@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t k_base = smem_u32(smem + L::kK + (tu % ST) * L::kTile);
         const uint32_t v_base = smem_u32(smem + L::kVp + tu % NU * 2 * L::kBox);
-        mma_kv_commit_w(tmem + (tu % NU == 0 ? L::kTU : L::kTS), sw128_desc_lo(k_base, D == 128 ? L::kBox : 0),
-                        sw128_desc_lo(v_base, L::kBox), kHi, idesc_u,
-                        u_full + tu % NU);
+        mma_kv_commit_w(tmem + (tu % NU == 0 ? L::kTU : L::kTS),
+                        sw128_desc_lo(k_base, D == 128 ? L::kBox : 0),
+                        sw128_desc_lo(v_base, L::kBox), kHi, idesc_u, u_full + tu % NU);
         if (!OUT) {
           mma_commit_w(qk_empty + tu % ST);
           mma_commit_w(pv_done + tu % VS);
@@ -481,6 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(done);
     const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
     mbar_wait_w(done, 0, drain);
+    // ... and every commit's arrival seen: nobody else waits for the last ones of these, and
+    // none may come when the CTA's shared memory is another's
+    const int nqk = OUT ? to : tu, npv = OUT ? tp : tu;
+    for (int u = max(0, nqk - ST); u < nqk; ++u)
+      mbar_wait_w(qk_empty + u % ST, (u / ST) & 1, drain);
+    for (int u = max(0, npv - VS); u < npv; ++u)
+      mbar_wait_w(pv_done + u % VS, (u / VS) & 1, drain);
   } else if (warp < kWarpV) {
     // ---------------------------------------------------------------- P = decayed, masked S
     if (OUT) {
