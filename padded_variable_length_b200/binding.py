@@ -456,19 +456,23 @@ class _Layout:
     """Of a tensor's shape and strides: the strides the library takes, (batch, token, head)
     and for single tokens (batch, head), and whether entries share memory.  A dimension of
     one entry is never stepped over: 0 is passed, whatever its stride is."""
-    __slots__ = ("shape", "strides", "strides2", "expanded")
+    __slots__ = ("shape", "dims", "strides", "strides2", "expanded", "dense")
 
     def __init__(self, shape, stride):
+        if not 2 <= len(shape) <= 4:
+            raise ValueError("expected a tensor of 3 or 4 dimensions")
         if stride[-1] != 1 and shape[-1] != 1:
             raise ValueError("the last dimension must be contiguous")
         s = [st if n > 1 else 0 for st, n in zip(stride, shape)][:-1]
-        self.shape = tuple(shape)
+        self.shape, self.dims = tuple(shape), len(shape)
+        self.dense = list(stride) == [math.prod(shape[i + 1:]) for i in range(len(shape))]
         self.strides = _I64x3(*([0] * (3 - len(s)) + s))
-        self.strides2 = _I64x2(*s[-2:])
+        self.strides2 = _I64x2(*([0] + s)[-2:])
         self.expanded = any(st == 0 and n > 1 for st, n in zip(stride, shape))
 
 
 _NO_STRIDES = _I64x3(0, 0, 0)
+_Tensor, _bf16, _f32, _empty_like = torch.Tensor, torch.bfloat16, torch.float32, torch.empty_like
 
 
 def _here() -> int:
@@ -481,20 +485,22 @@ def _here() -> int:
 
 def _tensor(t, name: str, dev: int, dims=(3, 4)) -> _Layout:
     """Layout of a bf16 tensor on device ``dev``, the last dimension contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() not in dims:
-        raise ValueError(f"{name} must be a bf16 tensor of {' or '.join(map(str, dims))} dimensions")
+    if not isinstance(t, _Tensor) or t.dtype is not _bf16:
+        raise ValueError(f"{name} must be a bf16 tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
     key = (t.shape, t.stride())
-    lay = _layouts.get(key)
-    return lay if lay is not None else _remember(_layouts, key, _Layout(*key))
+    lay = _layouts.get(key) or _remember(_layouts, key, _Layout(*key))
+    if lay.dims not in dims:
+        raise ValueError(f"{name} must have {' or '.join(map(str, dims))} dimensions")
+    return lay
 
 
 def _small(t, name: str, dtype, shape, dev: int) -> Optional[int]:
     """Pointer of a contiguous tensor of exactly this type and shape (None passes)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
@@ -504,9 +510,9 @@ def _small(t, name: str, dtype, shape, dev: int) -> Optional[int]:
 def _out(t: Optional[torch.Tensor], like: torch.Tensor, like_lay: _Layout, name: str, dev: int):
     """(output tensor, its layout): a new one, or the caller's after the checks it needs."""
     if t is None:
-        t = torch.empty_like(like)
-        return t, _tensor(t, name, dev)
-    lay = _tensor(t, name, dev, (like.dim(),))
+        t = _empty_like(like)
+        return t, like_lay if like_lay.dense else _tensor(t, name, dev)
+    lay = _tensor(t, name, dev, (like_lay.dims,))
     if lay.shape != like_lay.shape:
         raise ValueError(f"{name} must have shape {like_lay.shape}")
     if lay.expanded:
@@ -519,7 +525,8 @@ def _workspace(workspace, need: int, like: torch.Tensor, dev: int):
     if workspace is None:
         if need == 0:
             return None, None, 0
-        workspace = torch.empty((need + 3) // 4, dtype=torch.float32, device=like.device)
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the current CUDA device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -552,7 +559,7 @@ def _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, leng
             raise ValueError("a packed batch has no lengths: all of its rows are valid")
         lp = _small(lengths, "lengths", torch.int32, head[:1], dev)
     d = head[4:]
-    wqp, wkp = _small(wq, "wq", torch.float32, d, dev), _small(wk, "wk", torch.float32, d, dev)
+    wqp, wkp = _small(wq, "wq", _f32, d, dev), _small(wk, "wk", _f32, d, dev)
     rot = n_sec = sa = sb = 0
     sec = ip = pp = None
     if inv_freq is not None:
@@ -569,7 +576,7 @@ def _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, leng
                 raise ValueError(f"sections must be counts that add up to {pairs}")
             sec = _remember(_section_arrays, (pairs, key), (_i32 * len(counts))(*counts))
         n_sec = len(sec)
-        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or positions.get_device() != dev:
+        if not isinstance(positions, _Tensor) or positions.dtype is not torch.int32 or positions.get_device() != dev:
             raise ValueError("positions must be an int32 tensor on the current CUDA device")
         ps = positions.shape
         st = positions.stride()
@@ -637,7 +644,7 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
         dx, dxl = _out(dx, x, lay, "d" + name, dev)
         args.append((dy.data_ptr(), dyl.strides, dx.data_ptr(), dxl.strides))
         outs.append(dx)
-        grads.append(None if w is None else torch.empty_like(w))
+        grads.append(None if w is None else _empty_like(w))
     gq, gk = grads
     if not (head[0] and head[1] and head[2] + head[3]):
         return outs[0], outs[1], *(None if g is None else g.zero_() for g in grads)
@@ -681,10 +688,10 @@ def _linear_args(q, others, log_decay, lengths, cu_seqlens, max_seqlen, states, 
             raise ValueError("a padded batch takes lengths, no cu_seqlens or max_seqlen")
         (B, N), T = rows, 0
         lp = _small(lengths, "lengths", torch.int32, (B,), dev)
-    gp = _small(log_decay, "log_decay", torch.float32, (H,), dev)
+    gp = _small(log_decay, "log_decay", _f32, (H,), dev)
     if gp is None:
         raise ValueError("log_decay is needed")
-    ptrs = [_small(s, name, torch.float32, (B, H, d, d), dev) for s, name in states]
+    ptrs = [_small(s, name, _f32, (B, H, d, d), dev) for s, name in states]
     return (B, N, T, H, d, lp, cp, gp), ptrs, pairs, lay
 
 
@@ -746,11 +753,11 @@ def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] 
     B, H, d = ql.shape
     square = (B, H, d, d)
     lp = _small(lengths, "lengths", torch.int32, (B,), dev)
-    gp = _small(log_decay, "log_decay", torch.float32, (H,), dev)
-    sp = _small(state, "state", torch.float32, square, dev)
+    gp = _small(log_decay, "log_decay", _f32, (H,), dev)
+    sp = _small(state, "state", _f32, square, dev)
     if gp is None or sp is None:
         raise ValueError("log_decay and state are needed")
-    np_ = sp if state_out is None else _small(state_out, "state_out", torch.float32, square, dev)
+    np_ = sp if state_out is None else _small(state_out, "state_out", _f32, square, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, ol = _out(out, q, ql, "out", dev)

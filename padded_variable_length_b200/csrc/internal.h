@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "sigattn.h"
@@ -122,6 +123,24 @@ int cuda_status(cudaError_t e);
 
 // The limit of the kernels' bounded waits (sigattn_set_wait_limit_ns).
 unsigned long long wait_limit_ns();
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device.  `done` (one bit
+// per device, static beside the launch of that kernel) keeps later calls from asking again.
+template <class Kernel>
+int opt_in_shared(Kernel kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SIGATTN_ERR_NO_DEVICE;
+  }
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done->load(std::memory_order_relaxed) & bit) return SIGATTN_OK;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_status(e);
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return SIGATTN_OK;
+}
 
 // Device address of this device's status word (the record of bounded waits that gave up).
 int status_ptr(int** out);

@@ -949,9 +949,9 @@ int launch_one(const LinParams& p, cudaStream_t stream) {
   using L = LinLayout<D, OUT>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory");
   auto kern = linear_kernel<D, OUT>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-  if (e != cudaSuccess) return cuda_status(e);
+  static std::atomic<unsigned long long> opted{0};
+  const int rc = opt_in_shared(kern, L::kAlloc, &opted);
+  if (rc != SIGATTN_OK) return rc;
   kern<<<std::min(p.nitems, kSms), kThreads, L::kAlloc, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
@@ -994,11 +994,6 @@ int check_sizes(int B, int N, int64_t T, int H, int d, bool packed) {
 int fill(LinParams* p, int npass, int B, int N, int64_t T, int H, int d, const int32_t* lengths,
          const int32_t* cu, const float* log_decay, const TensorDesc* t, int n,
          const TensorDesc* out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return SIGATTN_ERR_NO_DEVICE;
-  }
   int rc;
   if ((rc = status_ptr(&p->status)) != SIGATTN_OK) return rc;
   for (int i = 0; i < n; ++i)

@@ -451,9 +451,9 @@ template <int D, int TURN, bool GRAD>
 int launch_turn(const QkParams& p, int blocks, cudaStream_t stream) {
   constexpr int bytes = kWarps * kDepth * sizeof(Slot<GRAD ? 4 : 2>);
   const auto kern = k_qk<D, TURN, GRAD>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return cuda_status(e);
+  static std::atomic<unsigned long long> opted{0};
+  const int rc = bytes > 48 * 1024 ? opt_in_shared(kern, bytes, &opted) : SIGATTN_OK;
+  if (rc != SIGATTN_OK) return rc;
   kern<<<blocks, kThreads, bytes, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
