@@ -440,7 +440,7 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * log_decay: device fp32 [H], at most 0 (above 0, or NaN, counts as 0; -inf is lambda = 0).
  * state: fp32 [B, H, d, d] (rows along k, columns along v), S before each sequence's first
  * token, or NULL for 0; final_state: the same layout, S after its last one (the state itself
- * for an empty sequence), or NULL.  They may be the same buffer.
+ * for an empty sequence), or NULL.  They may be the same buffer, but not overlap otherwise.
  *
  * Batches, like the attention calls' but without a plan: with cu_seqlens NULL, padded
  * [B, N, H, d] tensors, sequence b has lengths[b] rows (device int32 [B], clamped into
@@ -448,7 +448,9 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * included).  With cu_seqlens (device int32 [B + 1], non-decreasing; lengths must be NULL),
  * packed [T, H, d] tensors, sequence b in rows cu_seqlens[b] .. cu_seqlens[b + 1]; N is the
  * longest sequence (a longer one is cut there) and rows of no sequence are not written.
- * Pointers, strides and d (64, 128) as above; states and workspace 16-byte aligned.
+ * Pointers, strides and d (64, 128) as above; states and workspace 16-byte aligned.  Outputs
+ * must not overlap inputs or one another; an input's heads or tokens may share memory (stride
+ * 0), and each of them then has a gradient of its own.
  * Inputs are bf16 and accumulated in fp32; the state is kept in fp32.
  *
  * workspace: sigattn_linear_workspace_size() bytes (0 where B and H alone fill the GPU:
@@ -456,11 +458,11 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * not overlap on the GPU.  Results do not change from run to run.
  *
  * Backward of L = sum(do * o) + sum(dfinal_state * final_state): writes dq, dk, dv (bf16, pad
- * rows 0) and, where dstate is not NULL, dL/dstate (fp32).  dfinal_state NULL means 0;
- * dstate may be the same buffer as dfinal_state.  log_decay has no gradient.
+ * rows 0) and, where dstate is not NULL, dL/dstate (fp32).  dfinal_state NULL means 0.
+ * dstate must not overlap state or dfinal_state.  log_decay has no gradient.
  *
  * Errors: INVALID (null pointer, B, N, H or T < 1, both lengths and cu_seqlens, non-finite
- * scale, workspace missing or too small), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT,
+ * scale, workspace missing or too small, states that overlap where they must not), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT,
  * NO_DEVICE, CUDA; TIMEOUT through sigattn_get_status.
  */
 SIGATTN_API int sigattn_linear_workspace_size(int B, int N, int H, int d, int backward,

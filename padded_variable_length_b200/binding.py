@@ -520,12 +520,16 @@ def _out(t: Optional[torch.Tensor], like: torch.Tensor, like_lay: _Layout, name:
     return t, lay
 
 
-def _workspace(workspace, need: int, like: torch.Tensor, dev: int):
-    """(tensor, pointer, bytes): the caller's buffer, or a new one of `need` bytes."""
+def _workspace(workspace, need: int, like: torch.Tensor, dev: int, stream):
+    """(tensor, pointer, bytes): the caller's buffer, or a new one of `need` bytes, which must
+    not be handed out again before the call has run on a stream other than the current one."""
     if workspace is None:
         if need == 0:
             return None, None, 0
         workspace = like.new_empty(need, dtype=torch.uint8)
+        if stream is not None:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                    torch.cuda.ExternalStream(_stream(stream)))
         return workspace, workspace.data_ptr(), need
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the current CUDA device")
@@ -649,7 +653,7 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
     if not (head[0] and head[1] and head[2] + head[3]):
         return outs[0], outs[1], *(None if g is None else g.zero_() for g in grads)
     need = qk_norm_rope_bwd_workspace_bytes(head[0], head[1], head[4]) if gq is not None or gk is not None else 0
-    ws, wp, wn = _workspace(workspace, need, q if q is not None else k, dev)
+    ws, wp, wn = _workspace(workspace, need, q if q is not None else k, dev, stream)
     _check(_lib.sigattn_qk_norm_rope_bwd(*head, *_pair(q, ql), *_pair(k, kl), *args[0][:2], *args[1][:2], *rot,
                                          *args[0][2:], *args[1][2:], None if gq is None else gq.data_ptr(),
                                          None if gk is None else gk.data_ptr(), wp, wn, _stream(stream)),
@@ -695,6 +699,13 @@ def _linear_args(q, others, log_decay, lengths, cu_seqlens, max_seqlen, states, 
     return (B, N, T, H, d, lp, cp, gp), ptrs, pairs, lay
 
 
+def _hand_on(to: Optional[torch.Tensor], state: Optional[torch.Tensor]):
+    """Without tokens a state stays as it is (None: 0)."""
+    if to is not None and to is not state:
+        to.zero_() if state is None else to.copy_(state)
+    return to
+
+
 def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None,
                return_state: bool = False, scale: Optional[float] = None, out=None, final_state=None,
                workspace=None, stream=None):
@@ -713,7 +724,9 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
     if return_state and final_state is None:
         final_state = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
         fp = final_state.data_ptr()
-    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev)
+    if q.numel() == 0:
+        return out, _hand_on(final_state, state)
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev, stream)
     _check(_lib.sigattn_linear_fwd(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, wp, wn, _stream(stream)),
            "linear_fwd")
     return out, final_state
@@ -735,7 +748,9 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
     if state is not None and dstate_out is None:
         dstate_out = torch.empty_like(state)
         gp = dstate_out.data_ptr()
-    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev)
+    if q.numel() == 0:
+        return dq, dk, dv, _hand_on(dstate_out, dstate)
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev, stream)
     _check(_lib.sigattn_linear_bwd(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,
                                    dv.data_ptr(), dvl.strides, gp, wp, wn, _stream(stream)), "linear_bwd")
     return dq, dk, dv, dstate_out
@@ -761,6 +776,8 @@ def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] 
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     out, ol = _out(out, q, ql, "out", dev)
+    if q.numel() == 0:
+        return out
     _check(_lib.sigattn_linear_step(B, H, d, lp, gp, scale, q.data_ptr(), ql.strides2, k.data_ptr(), kl.strides2,
                                     v.data_ptr(), vl.strides2, sp, np_, out.data_ptr(), ol.strides2, _stream(stream)),
            "linear_step")

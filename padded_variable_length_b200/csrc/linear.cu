@@ -22,6 +22,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "internal.h"
@@ -969,6 +970,12 @@ int launch(const LinParams& p, cudaStream_t stream) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two state arrays of n floats share memory (absent ones share none).
+bool overlap(const float* a, const float* b, int64_t n) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return a && b && std::abs(x - y) < n * static_cast<int64_t>(sizeof(float));
+}
+
 int check_tensor(const void* ptr, const int64_t* strides, int rows, TensorDesc* t) {
   if (!ptr || !strides) return SIGATTN_ERR_INVALID;
   for (int i = 0; i < 3; ++i)
@@ -1063,6 +1070,9 @@ extern "C" int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const i
   if (need && (!workspace || workspace_bytes < need)) return SIGATTN_ERR_INVALID;
   if (!aligned16(state) || !aligned16(final_state) || !aligned16(workspace))
     return SIGATTN_ERR_ALIGNMENT;
+  // in place is fine: what writes an element of the state has read it before
+  if (state != final_state && overlap(state, final_state, static_cast<int64_t>(B) * H * d * d))
+    return SIGATTN_ERR_INVALID;
   LinParams p;
   std::memset(&p, 0, sizeof(p));
   if ((rc = fill(&p, 1, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 3, &to)) !=
@@ -1108,6 +1118,9 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
   if (need && (!workspace || workspace_bytes < need)) return SIGATTN_ERR_INVALID;
   if (!aligned16(state) || !aligned16(dfinal_state) || !aligned16(dstate) || !aligned16(workspace))
     return SIGATTN_ERR_ALIGNMENT;
+  // the other passes read them while this one is written
+  const int64_t n = static_cast<int64_t>(B) * H * d * d;
+  if (overlap(dstate, state, n) || overlap(dstate, dfinal_state, n)) return SIGATTN_ERR_INVALID;
   LinParams p;
   std::memset(&p, 0, sizeof(p));
   if ((rc = fill(&p, 3, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 4, out)) !=
@@ -1163,6 +1176,8 @@ extern "C" int sigattn_linear_step(int B, int H, int d, const int32_t* lengths,
   if (d != 64 && d != 128) return SIGATTN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(B) * H * (d / 32) > 0x7FFFFFFF) return SIGATTN_ERR_UNSUPPORTED;
   if (!aligned16(state) || !aligned16(state_out)) return SIGATTN_ERR_ALIGNMENT;
+  if (state != state_out && overlap(state, state_out, static_cast<int64_t>(B) * H * d * d))
+    return SIGATTN_ERR_INVALID;
   const auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
   StepParams p{H,
                lengths,

@@ -206,18 +206,84 @@ def test_packed_writes_only_its_rows_and_clamps():
     assert Bd.get_status() == 0 and torch.equal(o[:40], want[0][:40]) and torch.all(o[240:] == 5)
 
 
-def test_state_buffers_may_be_shared():
+def test_state_buffers_in_place():
+    """The final state may take the place of the starting one; the backward's three passes read
+    the states that they are given, so its dstate_out may not, and no call takes a part."""
     Bd = _bd()
-    for B, N in ((2, 200), (1, 1500)):
+    for B, N in ((2, 200), (100, 150), (1, 1500)):
         t = _make((B, N), 2, 64, B, True, seed=12)
         g = _slopes(2).cuda()
         o, fin = Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=t["state"], return_state=True)
-        *_, ds = Bd.linear_bwd(t["q"], t["k"], t["v"], t["do"], g, state=t["state"], dstate=t["dstate"])
-        s, e = t["state"].clone(), t["dstate"].clone()
+        s = t["state"].clone()
         o2, fin2 = Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=s, final_state=s)
-        *_, ds2 = Bd.linear_bwd(t["q"], t["k"], t["v"], t["do"], g, state=t["state"], dstate=e, dstate_out=e)
-        assert fin2 is s and ds2 is e
-        assert torch.equal(o, o2) and torch.equal(fin, fin2) and torch.equal(ds, ds2)
+        assert fin2 is s and torch.equal(o, o2) and torch.equal(fin, fin2)
+        for kw in (dict(dstate_out=t["dstate"]), dict(dstate_out=t["state"])):
+            with pytest.raises(Bd.SigattnError) as e:
+                Bd.linear_bwd(t["q"], t["k"], t["v"], t["do"], g, state=t["state"], dstate=t["dstate"], **kw)
+            assert e.value.code == -1
+        two = torch.zeros(2 * t["state"].numel(), device="cuda")
+        n = t["state"].numel()
+        part = lambda at: two[at:at + n].view_as(t["state"])
+        with pytest.raises(Bd.SigattnError):
+            Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=part(0), final_state=part(n // 2))
+        with pytest.raises(Bd.SigattnError):
+            Bd.linear_step(t["q"][:, 0], t["k"][:, 0], t["v"][:, 0], g, part(0), state_out=part(n // 2))
+        Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=part(0), final_state=part(n))
+    assert Bd.get_status() == 0
+
+
+def test_shared_heads_are_read_through_zero_strides():
+    """One key head for all query heads, as an expanded view: its gradient comes out per head,
+    the sum over the heads is the shared one's."""
+    Bd = _bd()
+    t = _make((2, 150), 3, 64, 2, False, seed=20)
+    one = t["k"][:, :, :1].contiguous()
+    wide = one.expand(-1, -1, 3, -1)
+    g = _slopes(3).cuda()
+    a = Bd.linear_fwd(t["q"], wide, t["v"], g)[0]
+    b = Bd.linear_fwd(t["q"], wide.contiguous(), t["v"], g)[0]
+    assert torch.equal(a, b)
+    ga = Bd.linear_bwd(t["q"], wide, t["v"], t["do"], g)
+    gb = Bd.linear_bwd(t["q"], wide.contiguous(), t["v"], t["do"], g)
+    assert all(torch.equal(x, y) for x, y in zip(ga[:3], gb[:3])) and ga[1].shape == wide.shape
+    assert Bd.get_status() == 0
+
+
+def test_without_tokens():
+    Bd = _bd()
+    g = _slopes(2).cuda()
+    s, e = torch.randn(3, 2, 64, 64, device="cuda"), torch.randn(3, 2, 64, 64, device="cuda")
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    where = dict(cu_seqlens=cu, max_seqlen=1)
+    o, fin = Bd.linear_fwd(q, q, q, g, state=s, return_state=True, **where)
+    *_, ds = Bd.linear_bwd(q, q, q, q, g, state=s, dstate=e, **where)
+    assert o.shape == q.shape and torch.equal(fin, s) and torch.equal(ds, e)
+    assert torch.all(Bd.linear_fwd(q, q, q, g, return_state=True, **where)[1] == 0)
+    assert Bd.linear_step(q, q, q, g, s[:0]).shape == q.shape
+
+
+def test_workspace_on_another_stream():
+    """A call given its stream keeps its workspace until it has run there, whatever the current
+    stream allocates meanwhile."""
+    Bd = _bd()
+    t = _make((1, 3000), 2, 128, 1, True, seed=21)
+    g = _slopes(2).cuda()
+    want = Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=t["state"], return_state=True)
+    need = Bd.linear_workspace_bytes(1, 3000, 2, 128)
+    assert need > 0
+    side = torch.cuda.Stream()
+    outs = []
+    torch.cuda.synchronize()
+    for i in range(8):
+        out, fin = torch.empty_like(want[0]), torch.empty_like(want[1])
+        Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=t["state"], out=out, final_state=fin,
+                      stream=side if i % 2 else side.cuda_stream)
+        torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        outs.append((out, fin))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
 
 
 @pytest.mark.parametrize("B,N,d", [(40, 300, 64), (2, 3000, 128)])
@@ -301,12 +367,14 @@ def test_prompt_then_tokens(d):
     assert whole.shape == (B, n + extra, H, d)
 
 
-def test_timeout_is_reported_and_leaves_the_next_call_sound():
-    """With a limit of 1 ns the kernel's waits give up, record it and end; nothing hangs."""
+@pytest.mark.parametrize("N,d", [(400, 64), (3000, 128)])
+def test_timeout_is_reported_and_leaves_the_next_call_sound(N, d):
+    """With a limit of 1 ns the kernels' waits give up, record it and end; nothing hangs."""
     Bd = _bd()
-    t = _make((2, 400), 2, 64, 2, True, seed=16)
+    t = _make((2, N), 2, d, 2, True, seed=16)
     g = _slopes(2).cuda()
-    run = lambda: Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=t["state"], return_state=True)
+    run = lambda: Bd.linear_fwd(t["q"], t["k"], t["v"], g, state=t["state"], return_state=True) + \
+        Bd.linear_bwd(t["q"], t["k"], t["v"], t["do"], g, state=t["state"], dstate=t["dstate"])
     want = run()
     assert Bd.get_status() == 0
     Bd.set_wait_limit_ns(1)
