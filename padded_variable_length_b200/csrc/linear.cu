@@ -23,7 +23,7 @@
 // alone.  A chunk is some 1800 cycles of tensor pipe, most of them spent fetching operands from
 // shared memory, and the jobs between one product and the next hang on each other: with all of
 // their arithmetic taken out the long ragged batch (8 x 4096..16384, 16 heads of 128) takes 278
-// us, with it 335, and the copy of its tensors 233.
+// us, with it 330, and the copy of its tensors 233.
 // Layout: 128 tokens a chunk are the M of every product; d = 128 is cut into two items of 64
 // value columns, because all of its operands fit shared memory twice that way (one item of 128
 // columns leaves K and Q single stages, whose copies nothing hides: 553 us).
@@ -48,8 +48,9 @@ constexpr int kSms = 148;       // B200
 constexpr int kMaxSorted = 256;  // batches up to this size are walked longest-first
 constexpr int kRing = 8;         // work items decoded ahead
 constexpr int kMaxSegs = 16;     // of a sequence
-constexpr int kThreads = 736;
-// first warps of P (4), V' (4), the outputs (4) and the state (8); last, the items' (1)
+constexpr int kThreads = 768;
+// first warps of P (4), V' (4), the outputs (4), the state (8); last, those of the items and of
+// the zero rows
 constexpr int kWarpP = 2, kWarpV = 6, kWarpO = 10, kWarpS = 14, kWarpI = 22;
 
 struct LinPass {
@@ -271,8 +272,10 @@ __device__ __forceinline__ void weigh_near(const uint32_t (&s)[16], float l2, bo
 // OUT: the whole computation.  Otherwise only the state that each segment of a sequence
 // leaves from a zero start is computed, into pass.seg.
 //
-// Warps: 0 copies, 1 issues the products, then four jobs on a chunk, each with warps of its
-// own so that none waits for another's turn:
+// Warps: 0 copies, 1 issues the products, the last two decode the work items and zero the pad
+// rows (at their own pace: written by the outputs' warps after an item's last chunk they held
+// the next item back, 341 us instead of 330 on the long ragged batch); and four jobs on a chunk,
+// each with warps of its own so that none waits for another's turn:
 //   P       S from TMEM, decayed, masked and rounded into the A operand of P V
 //   V'      the decayed values, as the sum of two bf16 numbers: rounded once they would cost
 //           the outputs a third rounding (2.6e-3 off instead of 2.3e-3, where one rounding is
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, OUT ? 21 : 17);  // the warps that take items
+      mbar_init(item_empty + i, OUT ? (p.cu ? 21 : 22) : 17);  // the warps that take items
     }
     *abort_flag = 0;
     *drain_flag = 0;
@@ -686,27 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
         }
-        if (ok && !p.cu) {
-          // Rows behind the last chunk of a padded sequence, within the item's segment, are 0
-          // (those inside it came out of the chunk as 0).
-          const int lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk) + wq * 32;
-          const int hi = it.seg == p.nseg - 1 ? p.N
-                                              : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
-          if (lo < hi) {
-            if (lane == 0) bulk_wait_read_0();
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              *reinterpret_cast<uint4*>(box + x * 512 + lane * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              for (int row = lo; row < hi; row += kChunk)
-                tma_store_4d(p.map + ps.o, box, it.slice * kCols, row, it.h, it.s.tma_b);
-              bulk_commit_group();
-            }
-          }
-        }
       }
       if (lane == 0) bulk_wait_all();
       __syncwarp();
@@ -789,6 +771,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kHold; c += 4)
           *reinterpret_cast<float4*>(dst + c) = make_float4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+      }
+    }
+  } else if (warp == kWarpI + 1) {
+    // ---------------------------------------------------------------- zero rows
+    // Rows behind a padded sequence's last chunk, within the item's segment, are written as 0
+    // (those inside it come out of the chunk as 0).
+    if (OUT && !p.cu) {
+      Item it;
+      for (int k = 0; take(k, it); ++k) {
+        const LinPass& ps = p.pass[it.pass];
+        const int lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk);
+        const int hi = it.seg == p.nseg - 1 ? p.N : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
+        __nv_bfloat16* out =
+            ps.out + it.b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols + lane % 8 * 8;
+        for (int r = lo + lane / 8; r < hi; r += 4)
+          *reinterpret_cast<uint4*>(out + r * ps.o_sn) = make_uint4(0u, 0u, 0u, 0u);
       }
     }
   } else {
