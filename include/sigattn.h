@@ -449,8 +449,11 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * packed [T, H, d] tensors, sequence b in rows cu_seqlens[b] .. cu_seqlens[b + 1]; N is the
  * longest sequence (a longer one is cut there) and rows of no sequence are not written.
  * Pointers, strides and d (64, 128) as above; states and workspace 16-byte aligned.  Outputs
- * must not overlap inputs or one another; an input's heads or tokens may share memory (stride
- * 0), and each of them then has a gradient of its own.
+ * must not overlap inputs or one another (the very same pointer is refused); an input's heads
+ * or tokens may share memory (stride 0), and each of them then has a gradient of its own.
+ * Valid rows are expected to be finite: an infinity or a NaN in v (backward: in k, q or do)
+ * makes that column of its 128 tokens (counted from the sequence's first) NaN, earlier ones
+ * included.
  * Inputs are bf16 and accumulated in fp32; the state is kept in fp32.
  *
  * workspace: sigattn_linear_workspace_size() bytes (0 where B and H alone fill the GPU:
@@ -462,8 +465,9 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * dstate must not overlap state or dfinal_state.  log_decay has no gradient.
  *
  * Errors: INVALID (null pointer, B, N, H or T < 1, both lengths and cu_seqlens, non-finite
- * scale, workspace missing or too small, states that overlap where they must not), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT,
- * NO_DEVICE, CUDA; TIMEOUT through sigattn_get_status.
+ * scale, workspace missing or too small, states that overlap where they must not, an output
+ * that is an input), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT, NO_DEVICE, CUDA; TIMEOUT
+ * through sigattn_get_status.
  */
 SIGATTN_API int sigattn_linear_workspace_size(int B, int N, int H, int d, int backward,
                                               size_t* bytes);

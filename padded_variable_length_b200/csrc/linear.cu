@@ -34,6 +34,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 
 #include "internal.h"
 #include "sm100.cuh"
@@ -986,6 +987,12 @@ bool overlap(const float* a, const float* b, int64_t n) {
   return a && b && std::abs(x - y) < n * static_cast<int64_t>(sizeof(float));
 }
 
+// Whether an output is the very tensor that one of the others is: what reads them is not done
+// when the first output is written (two items share the rows of q and k, passes the inputs).
+bool same_as_any(const void* out, std::initializer_list<const void*> others) {
+  return std::find(others.begin(), others.end(), out) != others.end();
+}
+
 int check_tensor(const void* ptr, const int64_t* strides, int rows, TensorDesc* t) {
   if (!ptr || !strides) return SIGATTN_ERR_INVALID;
   for (int i = 0; i < 3; ++i)
@@ -1083,6 +1090,7 @@ extern "C" int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const i
   // in place is fine: what writes an element of the state has read it before
   if (state != final_state && overlap(state, final_state, static_cast<int64_t>(B) * H * d * d))
     return SIGATTN_ERR_INVALID;
+  if (same_as_any(o, {q, k, v})) return SIGATTN_ERR_INVALID;
   LinParams p;
   std::memset(&p, 0, sizeof(p));
   if ((rc = fill(&p, 1, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 3, &to)) !=
@@ -1131,6 +1139,9 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
   // the other passes read them while this one is written
   const int64_t n = static_cast<int64_t>(B) * H * d * d;
   if (overlap(dstate, state, n) || overlap(dstate, dfinal_state, n)) return SIGATTN_ERR_INVALID;
+  if (same_as_any(dq, {q, k, v, dout, dk, dv}) || same_as_any(dk, {q, k, v, dout, dv}) ||
+      same_as_any(dv, {q, k, v, dout}))
+    return SIGATTN_ERR_INVALID;
   LinParams p;
   std::memset(&p, 0, sizeof(p));
   if ((rc = fill(&p, 3, B, N, T, H, d, lengths, cu_seqlens, log_decay, t, 4, out)) !=
@@ -1188,6 +1199,7 @@ extern "C" int sigattn_linear_step(int B, int H, int d, const int32_t* lengths,
   if (!aligned16(state) || !aligned16(state_out)) return SIGATTN_ERR_ALIGNMENT;
   if (state != state_out && overlap(state, state_out, static_cast<int64_t>(B) * H * d * d))
     return SIGATTN_ERR_INVALID;
+  if (same_as_any(o, {q, k, v})) return SIGATTN_ERR_INVALID;
   const auto bf = [](const void* x) { return static_cast<const __nv_bfloat16*>(x); };
   StepParams p{H,
                lengths,

@@ -107,3 +107,18 @@ def test_binding_refuses_before_calling():
         Bd.linear_step(q[:, 0], q[:, 0], q[:, 0], g, torch.zeros(2, 2, 64, 64))
     with pytest.raises(ValueError):
         Bd.linear_step(q, q, q, g, torch.zeros(2, 2, 64, 64))
+
+
+@pytest.mark.parametrize("same", ["q", "k", "v"])
+def test_linear_output_that_is_an_input_is_refused(same):
+    at = {n: P(1 << 20 | i << 12) for i, n in enumerate(("q", "k", "v", "do", "dq", "dk", "dv"))}
+    t = lambda n: (at[n], OKS)
+    assert Bd.lib.sigattn_linear_fwd(2, 8, 0, 2, 64, None, None, P(16), 1.0, *t("q"), *t("k"), *t("v"), None, at[same], OKS,
+                                     None, None, 0, None) == INVALID
+    assert Bd.lib.sigattn_linear_step(2, 2, 64, None, P(16), 1.0, at["q"], S2(1, 1), at["k"], S2(1, 1), at["v"], S2(1, 1),
+                                      P(16), P(16), at[same], S2(1, 1), None) == INVALID
+    for out in ("dq", "dk", "dv"):
+        for other in (same, "do", *({"dq", "dk", "dv"} - {out})):
+            outs = [at[other] if n == out else at[n] for n in ("dq", "dk", "dv")]
+            assert Bd.lib.sigattn_linear_bwd(2, 8, 0, 2, 64, None, None, P(16), 1.0, *t("q"), *t("k"), *t("v"), *t("do"), None,
+                                             None, outs[0], OKS, outs[1], OKS, outs[2], OKS, None, None, 0, None) == INVALID
