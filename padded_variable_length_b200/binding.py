@@ -724,7 +724,7 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
     if return_state and final_state is None:
         final_state = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
         fp = final_state.data_ptr()
-    if q.numel() == 0:
+    if N == 0 or q.numel() == 0:
         return out, _hand_on(final_state, state)
     ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev, stream)
     _check(_lib.sigattn_linear_fwd(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, wp, wn, _stream(stream)),
@@ -748,7 +748,7 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
     if state is not None and dstate_out is None:
         dstate_out = torch.empty_like(state)
         gp = dstate_out.data_ptr()
-    if q.numel() == 0:
+    if N == 0 or q.numel() == 0:
         return dq, dk, dv, _hand_on(dstate_out, dstate)
     ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev, stream)
     _check(_lib.sigattn_linear_bwd(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,

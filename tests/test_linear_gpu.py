@@ -263,6 +263,21 @@ def test_without_tokens():
     assert Bd.linear_step(q, q, q, g, s[:0]).shape == q.shape
 
 
+def test_packed_rows_of_no_sequence_alone():
+    """max_seqlen = 0, all sequences empty: the states go through, the rows stay as they are."""
+    Bd = _bd()
+    g = _slopes(2).cuda()
+    s = torch.randn(3, 2, 64, 64, device="cuda")
+    q = torch.randn(5, 2, 64, device="cuda").to(torch.bfloat16)
+    where = dict(cu_seqlens=torch.zeros(4, dtype=torch.int32, device="cuda"), max_seqlen=0)
+    out = torch.full_like(q, 7.0)
+    _, fin = Bd.linear_fwd(q, q, q, g, state=s, return_state=True, out=out, **where)
+    *_, ds = Bd.linear_bwd(q, q, q, q, g, state=s, dstate=s, **where)
+    assert torch.equal(fin, s) and torch.equal(ds, s) and torch.all(out == 7.0)
+    with pytest.raises(Bd.SigattnError):
+        Bd.linear_fwd(q, q, q, g, cu_seqlens=where["cu_seqlens"], max_seqlen=-1)
+
+
 def test_workspace_on_another_stream():
     """A call given its stream keeps its workspace until it has run there, whatever the current
     stream allocates meanwhile."""
