@@ -13,8 +13,11 @@ Modules
   brute      pure-Python loops for tiny shapes (a second, independent spelling)
   tiles      the 128 x 128 tile list (CSR / CSC / kinds / partial bitmasks) by
              brute-force any/all over each block
+  qknorm     norm of query and key heads with the position rotation, and gradients
+  linear     linear attention with a decay per head, token by token, and gradients
 
-Pinning: every function here is checked in ``tests/test_oracle_pins.py`` against
+Pinning: every function here is checked in ``tests/test_oracle_pins.py`` (the last
+two modules in ``tests/test_oracle_qknorm_linear.py``) against
 closed forms, brute force, finite differences and invariants derived from the
 pages ("Better Models, Faster Training: Sigmoid Attention for single-cell
 Foundation Models"; "Binary Block Masking"; the softmax_1 / QuietAttention
