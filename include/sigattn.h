@@ -454,7 +454,9 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * Valid rows are expected to be finite: an infinity or a NaN in v (backward: in k, q or do)
  * makes that column of its 128 tokens (counted from the sequence's first) NaN, earlier ones
  * included.
- * Inputs are bf16 and accumulated in fp32; the state is kept in fp32.
+ * Inputs are bf16 and accumulated in fp32; the state is kept in fp32.  What enters it is
+ * rounded to 16 bits where a state is handed out (final_state, dstate) and to bf16 where it
+ * only serves the outputs, so these differ a little between the two calls.
  *
  * workspace: sigattn_linear_workspace_size() bytes (0 where B and H alone fill the GPU:
  * then it may be NULL), contents free on entry and undefined after; calls sharing one must

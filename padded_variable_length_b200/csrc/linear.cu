@@ -19,11 +19,12 @@
 //   o_i = lambda^r R^T q_i + sum_{j >= i} lambda^(j-i) (..),  R <- lambda^m R + sum_j lambda^(j+1) k_j v_j^T
 //
 // What it has to move: q, k, v and o once (the backward seven tensors; its passes read ten, the
-// two that run side by side sharing their reads through L2).  What bounds it: not the memory
-// alone.  A chunk is some 1800 cycles of tensor pipe, most of them spent fetching operands from
-// shared memory, and the jobs between one product and the next hang on each other: with all of
-// their arithmetic taken out the long ragged batch (8 x 4096..16384, 16 heads of 128) takes 278
-// us, with it 330, and the copy of its tensors 233.
+// two that run side by side sharing their reads through L2).  What bounds it is shared memory's
+// 128 bytes a cycle: for a chunk of d = 128 (64 of the value columns) 80 KB come in, the products
+// fetch 64 (S), 16 (P V), 48 (Q R) and 48 KB (K^T V', 64 with a V' of two numbers), V' takes 32
+// (48), R 16 and the outputs 32: 2690 cycles (2940).  The long ragged batch (8 x 4096..16384, 16
+// heads of 128), 153 chunks on the fullest SM, takes 303 us (328), 3800 cycles each; the copy of
+// its tensors 233.
 // Layout: 128 tokens a chunk are the M of every product; d = 128 is cut into two items of 64
 // value columns, because all of its operands fit shared memory twice that way (one item of 128
 // columns leaves K and Q single stages, whose copies nothing hides: 553 us).
@@ -145,7 +146,7 @@ __device__ __forceinline__ int valid_of(const Item& it, int c) {
   return min(kChunk, it.s.n - c * kChunk);
 }
 
-template <int D, bool OUT>
+template <int D, bool OUT, bool TWO>
 struct LinLayout {
   static constexpr int kBoxes = D / 64;
   static constexpr int kBox = 128 * 128;            // 128 tokens x 64 bf16
@@ -153,13 +154,14 @@ struct LinLayout {
   // Stages of Q and K, and of V.  Without the outputs there are no Q, R and O, and their room
   // goes to stages and a second V'.
   static constexpr int kSt = OUT ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
-  static constexpr int kVs = OUT ? (D == 64 ? 4 : 2) : (D == 64 ? 4 : 3);
+  static constexpr int kVs = OUT ? (D == 64 ? 4 : TWO ? 2 : 3) : (D == 64 ? 4 : 3);
   static constexpr int kNu = OUT ? 1 : 2;           // buffers of V' and U
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kSt * kTile;
   static constexpr int kV = kQ + (OUT ? kSt * kTile : 0);
-  static constexpr int kVp = kV + kVs * kBox;       // V' and, behind it, its rounding error
-  static constexpr int kR = kVp + kNu * 2 * kBox;   // bf16 state, D rows of 64
+  static constexpr int kVp = kV + kVs * kBox;       // V' and (TWO) behind it its rounding error
+  static constexpr int kVpSize = TWO ? 2 * kBox : kBox;
+  static constexpr int kR = kVp + kNu * kVpSize;   // bf16 state, D rows of 64
   static constexpr int kO = kR + (OUT ? D * 128 : 0);  // outputs on their way, 4 KB per warp
   static constexpr int kBar = kO + (OUT ? kBox : 0);
   // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2]
@@ -272,21 +274,25 @@ __device__ __forceinline__ void weigh_near(const uint32_t (&s)[16], float l2, bo
 
 // OUT: the whole computation.  Otherwise only the state that each segment of a sequence
 // leaves from a zero start is computed, into pass.seg.
+// TWO: V' is carried as the sum of two bf16 numbers, because a state is handed out, whose fp32
+// accuracy a rounded V' would cost (2^-9 instead of 2^-18).  Where the state only serves the
+// outputs, for which it is rounded to bf16 anyway, V' is rounded once: the outputs are 2.6e-3
+// off instead of 2.3e-3 (relative, 2-norm; their own rounding is 1.7e-3), the long ragged batch
+// takes 303 us instead of 328, gradients of 64 documents (32768 tokens, 16 heads of 128) 357
+// instead of 430.
 //
 // Warps: 0 copies, 1 issues the products, the last two decode the work items and zero the pad
 // rows (at their own pace: written by the outputs' warps after an item's last chunk they held
 // the next item back, 341 us instead of 330 on the long ragged batch); and four jobs on a chunk,
 // each with warps of its own so that none waits for another's turn:
 //   P       S from TMEM, decayed, masked and rounded into the A operand of P V
-//   V'      the decayed values, as the sum of two bf16 numbers: rounded once they would cost
-//           the outputs a third rounding (2.6e-3 off instead of 2.3e-3, where one rounding is
-//           1.7e-3) and the fp32 states their accuracy (2^-9 instead of 2^-18)
+//   V'      the decayed values, rounded once or as the sum of two bf16 numbers
 //   O       lambda^(i+1) Q R + P V to bf16 and out, a tensor-map store of 32 rows per warp
 //   state   R <- lambda^m R + K^T V' in registers; its bf16 copy is the B operand of Q R
-template <int D, bool OUT>
+template <int D, bool OUT, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ LinParams p) {
-  using L = LinLayout<D, OUT>;
+  using L = LinLayout<D, OUT, TWO>;
   constexpr int ST = L::kSt, VS = L::kVs;
   constexpr int NU = L::kNu;
   extern __shared__ uint8_t smem_raw[];
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kHi = sw128_desc_hi(1024);
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, kCols, true);
-    constexpr uint32_t idesc_u = idesc_bf16_f32(128, 2 * kCols, true, true);
+    constexpr uint32_t idesc_u = idesc_bf16_f32(128, TWO ? 2 * kCols : kCols, true, true);
     int total = 0;
     for (int k = lane; snake_item(k) < p.nitems; k += 32)
       total += decode<D>(p, order, snake_item(k)).cn;
@@ -460,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // for d = 64 the chunk stride of 0 gives them twice, lanes 64-127 a copy of 0-63.
         tc_fence_after();
         const uint32_t k_base = smem_u32(smem + L::kK + (tu % ST) * L::kTile);
-        const uint32_t v_base = smem_u32(smem + L::kVp + tu % NU * 2 * L::kBox);
+        const uint32_t v_base = smem_u32(smem + L::kVp + tu % NU * L::kVpSize);
         mma_kv_commit_w(tmem + (tu % NU == 0 ? L::kTU : L::kTS),
                         sw128_desc_lo(k_base, D == 128 ? L::kBox : 0),
                         sw128_desc_lo(v_base, L::kBox), kHi, idesc_u, u_full + tu % NU);
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (m < kChunk && !(ok = mbar_wait_w(qk_full + s, (t / ST) & 1, wctx))) break;
         // 16 bytes a step, at the address they have in the swizzled tile: only its row counts
         uint8_t* v = smem + L::kV + vs * L::kBox + tid * 16;
-        uint8_t* vp = smem + L::kVp + t % NU * 2 * L::kBox + tid * 16;
+        uint8_t* vp = smem + L::kVp + t % NU * L::kVpSize + tid * 16;
         const int row0 = tid / 8;
         if (m < kChunk) {
           // Behind the sequence: whatever these rows hold (NaN among it) must not reach the
@@ -613,14 +619,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                 __uint_as_float(wds[y] & 0xFFFF0000u)),
                                     make_float2(f, f));
               hi[y] = pack_bf16x2(a.x, a.y);
-              const float2 b = fma2(make_float2(__uint_as_float(hi[y] << 16),
-                                                __uint_as_float(hi[y] & 0xFFFF0000u)),
-                                    make_float2(-1.0f, -1.0f), a);
-              lo[y] = pack_bf16x2(b.x, b.y);
+              if constexpr (TWO) {
+                const float2 b = fma2(make_float2(__uint_as_float(hi[y] << 16),
+                                                  __uint_as_float(hi[y] & 0xFFFF0000u)),
+                                      make_float2(-1.0f, -1.0f), a);
+                lo[y] = pack_bf16x2(b.x, b.y);
+              }
             }
             uint8_t* dst = vp + (x0 + x) * 2048;
             *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + L::kBox) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if constexpr (TWO)
+              *reinterpret_cast<uint4*>(dst + L::kBox) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         fence_proxy_async_smem();
@@ -712,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool rev = ps.reverse != 0;
       const int64_t bh = static_cast<int64_t>(it.b) * p.H + it.h;
       float* seg = ps.seg + ((bh * p.nseg + it.seg) * D + row) * D + it.slice * kCols + col0;
-      if (OUT && p.nseg > 1) {
+      if (!TWO && p.nseg > 1) {
         if (it.cn > 0)
 #pragma unroll
           for (int c = 0; c < kHold; c += 4) {
@@ -754,20 +763,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kHold; c += 8) {
           uint32_t u[8], e[8];
           tmem_ld8(t_lane + at + c, u);
-          tmem_ld8(t_lane + at + kCols + c, e);
+          if constexpr (TWO) tmem_ld8(t_lane + at + kCols + c, e);
           tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 8; ++x)
-            r[c + x] = fmaf(f, r[c + x], __uint_as_float(u[x]) + __uint_as_float(e[x]));
+            r[c + x] = fmaf(f, r[c + x],
+                            TWO ? __uint_as_float(u[x]) + __uint_as_float(e[x])
+                                : __uint_as_float(u[x]));
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(u_empty + t % NU);
       }
+      if constexpr (!TWO) continue;
       float* dst = !OUT ? (it.cn > 0 ? seg : nullptr)
-                   : (p.nseg == 1 && ps.fin)
-                       ? ps.fin + (bh * D + row) * D + it.slice * kCols + col0
-                       : nullptr;
+                   : ps.fin ? ps.fin + (bh * D + row) * D + it.slice * kCols + col0 : nullptr;
       if (ok && dst) {
 #pragma unroll
         for (int c = 0; c < kHold; c += 4)
@@ -956,11 +966,11 @@ void segments(int npass, int B, int N, int H, int d, int* nseg, int* seg_chunks)
   *nseg = (chunks + *seg_chunks - 1) / *seg_chunks;
 }
 
-template <int D, bool OUT>
+template <int D, bool OUT, bool TWO>
 int launch_one(const LinParams& p, cudaStream_t stream) {
-  using L = LinLayout<D, OUT>;
+  using L = LinLayout<D, OUT, TWO>;
   static_assert(L::kAlloc <= 227 * 1024, "shared memory");
-  auto kern = linear_kernel<D, OUT>;
+  auto kern = linear_kernel<D, OUT, TWO>;
   static std::atomic<unsigned long long> opted{0};
   const int rc = opt_in_shared(kern, L::kAlloc, &opted);
   if (rc != SIGATTN_OK) return rc;
@@ -971,12 +981,14 @@ int launch_one(const LinParams& p, cudaStream_t stream) {
 template <int D>
 int launch(const LinParams& p, cudaStream_t stream) {
   if (p.nseg > 1) {
-    int rc = launch_one<D, false>(p, stream);
+    int rc = launch_one<D, false, true>(p, stream);
     if (rc != SIGATTN_OK) return rc;
     k_linear_join<D><<<dim3(D * D / 512, p.B * p.H, p.npass), 128, 0, stream>>>(p);
     if ((rc = cuda_status(cudaGetLastError())) != SIGATTN_OK) return rc;
   }
-  return launch_one<D, true>(p, stream);
+  bool two = false;
+  for (int i = 0; i < p.npass; ++i) two = two || (p.nseg == 1 && p.pass[i].fin);
+  return two ? launch_one<D, true, true>(p, stream) : launch_one<D, true, false>(p, stream);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
