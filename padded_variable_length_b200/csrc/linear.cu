@@ -20,11 +20,14 @@
 //
 // What it has to move: q, k, v and o once (the backward seven tensors; its passes read ten, the
 // two that run side by side sharing their reads through L2).  What bounds it is shared memory's
-// 128 bytes a cycle: for a chunk of d = 128 (64 of the value columns) 80 KB come in, the products
-// fetch 64 (S), 16 (P V), 48 (Q R) and 48 KB (K^T V', 64 with a V' of two numbers), V' takes 32
-// (48), R 16 and the outputs 32: 2690 cycles (2940).  The long ragged batch (8 x 4096..16384, 16
-// heads of 128), 153 chunks on the fullest SM, takes 303 us (328), 3800 cycles each; the copy of
-// its tensors 233.
+// 128 bytes a cycle and waiting.  For a chunk of d = 128 (64 of the value columns) 80 KB come
+// in, the products fetch 64 (S), 16 (P V), 48 (Q R) and 48 KB (K^T V'; 64 with a V' of two
+// numbers), V' takes 32 (48), R 16 and the outputs 32: 2690 cycles (2940).  The long ragged batch
+// (8 x 4096..16384, 16 heads of 128), 153 chunks on the fullest SM, takes 292 us, 3600 cycles
+// each; the copy of its tensors 233.  The rest is a chunk's jobs that wait for one another, and
+// its loads for the products that free their stage: with Q R in two buffers, so that it need not
+// wait for the outputs of the chunk before, and the issuer's tests side by side, that batch went
+// from 303 to 292 us and the gradients of the documents below from 335 to 316.
 // Layout: 128 tokens a chunk are the M of every product; d = 128 is cut into two items of 64
 // value columns, because all of its operands fit shared memory twice that way (one item of 128
 // columns leaves K and Q single stages, whose copies nothing hides: 553 us).
@@ -156,6 +159,7 @@ struct LinLayout {
   static constexpr int kSt = OUT ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
   static constexpr int kVs = OUT ? (D == 64 ? 4 : TWO ? 2 : 3) : (D == 64 ? 4 : 3);
   static constexpr int kNu = OUT ? 1 : 2;           // buffers of V' and U
+  static constexpr int kNo = TWO ? 1 : 2;           // buffers of Q R
   static constexpr int kK = 0;
   static constexpr int kQ = kK + kSt * kTile;
   static constexpr int kV = kQ + (OUT ? kSt * kTile : 0);
@@ -165,8 +169,8 @@ struct LinLayout {
   static constexpr int kO = kR + (OUT ? D * 128 : 0);  // outputs on their way, 4 KB per warp
   static constexpr int kBar = kO + (OUT ? kBox : 0);
   // qk_full[St] qk_empty[St] v_full[Vs] pv_done[Vs] s_full[2] p_full[2]
-  // u_full[2] u_empty[2] vp_full[2] r_full o_empty done item_full[8] item_empty[8]
-  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 13 + 2 * kRing;
+  // u_full[2] u_empty[2] vp_full[2] o_empty[2] r_full done item_full[8] item_empty[8]
+  static constexpr int kNumBars = 2 * kSt + 2 * kVs + 14 + 2 * kRing;
   static constexpr int kMisc = (kBar + 8 * kNumBars + 15) / 16 * 16;  // tmem base, flags
   static constexpr int kPow = kMisc + 16;            // powers of lambda, 32 per warp of P
   static constexpr int kItems = kPow + 4 * 32 * 4;   // work items decoded ahead
@@ -175,9 +179,10 @@ struct LinLayout {
   static constexpr int kAlloc = kBytes + 1024;       // slack for 1024-byte alignment
   // TMEM columns
   static constexpr int kTS = 0;     // two S / P buffers of 128
-  static constexpr int kTO1 = 256;  // Q R
-  static constexpr int kTO2 = 320;  // P V
-  static constexpr int kTU = 384;   // K^T V', then K^T times its rounding error
+  static constexpr int kTO2 = 256;  // P V
+  static constexpr int kTO1 = 320;  // Q R
+  // K^T V' and (TWO) K^T times its rounding error
+  static constexpr int kTU = kTO1 + kNo * kCols;
 };
 
 // Products of a chunk with the commit behind them, all issued under one elect.sync (see
@@ -229,29 +234,38 @@ __device__ __forceinline__ void mma_kv_commit_w(uint32_t d_tmem, uint32_t a_lo, 
 #undef SIGATTN_LIN_HEAD
 #undef SIGATTN_LIN_TAIL
 
-// lambda^|i - j| in blocks of 32 columns: off the diagonal the product of a row's power f up
-// to the block's near end and a column's power pow[c] from there, both at most 1 for any
-// decay; in the diagonal block, where that split would overflow, exp2 of each element.
+// lambda^|i - j| in blocks of 32 columns is the product of a row's power f up to the block's
+// near end and a column's power pow[c] from there.  Off the diagonal both are at most 1 for any
+// decay; in the diagonal block f is lambda^-31 at most, 2^62 where lambda is 1/4 or more; below
+// that each element takes an exp2 of its own (weigh_near).
 
-// 32 columns of a row of S off the diagonal.  Columns from `last` on are behind the sequence.
-__device__ __forceinline__ void weigh_far(const uint32_t (&s)[32], float f, const float* pow,
-                                          int last, uint32_t (&pk)[16]) {
+// Waits for the reads of TMEM; r, one of them, is not used before (which the compiler could not
+// know when the read and its use are in different steps of a loop).
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+// 16 columns of a row of S.  masked: bit c of keep says whether column c counts.
+__device__ __forceinline__ void weigh(const uint32_t (&s)[16], float f, const float* pow,
+                                      bool masked, uint32_t keep, uint32_t (&pk)[8]) {
   const float2 f2 = make_float2(f, f);
 #pragma unroll
-  for (int c = 0; c < 32; c += 4) {
+  for (int c = 0; c < 16; c += 4) {
     const float4 q = *reinterpret_cast<const float4*>(pow + c);
-    const float2 a = mul2(mul2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), f2),
-                          make_float2(q.x, q.y));
-    const float2 b =
-        mul2(mul2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), f2),
-             make_float2(q.z, q.w));
+    const float2 a = mul2(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])),
+                          mul2(f2, make_float2(q.x, q.y)));
+    const float2 b = mul2(make_float2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])),
+                          mul2(f2, make_float2(q.z, q.w)));
     pk[c / 2] = pack_bf16x2(a.x, a.y);
     pk[c / 2 + 1] = pack_bf16x2(b.x, b.y);
   }
-  if (last < 32) {
+  if (masked) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      pk[c] &= (2 * c < last ? 0xFFFFu : 0u) | (2 * c + 1 < last ? 0xFFFF0000u : 0u);
+    for (int c = 0; c < 8; ++c)
+      pk[c] &= (keep >> 2 * c & 1u ? 0xFFFFu : 0u) | (keep >> 2 * c & 2u ? 0xFFFF0000u : 0u);
   }
 }
 
@@ -309,9 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* u_full = p_full + 2;       // K^T V' complete: U ready, V' free
   uint64_t* u_empty = u_full + 2;
   uint64_t* vp_full = u_empty + 2;
-  uint64_t* r_full = vp_full + 2;
-  uint64_t* o_empty = r_full + 1;
-  uint64_t* done = o_empty + 1;
+  uint64_t* o_empty = vp_full + 2;     // outputs read from TMEM
+  uint64_t* r_full = o_empty + 2;
+  uint64_t* done = r_full + 1;
   uint64_t* item_full = done + 1;
   uint64_t* item_empty = item_full + kRing;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
@@ -336,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(u_full + i, 1);
       mbar_init(u_empty + i, 8);
       mbar_init(vp_full + i, 4);
+      mbar_init(o_empty + i, 4);
     }
     mbar_init(r_full, 8);
-    mbar_init(o_empty, 4);
     mbar_init(done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(item_full + i, 1);
@@ -431,40 +445,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = lane; snake_item(k) < p.nitems; k += 32)
       total += decode<D>(p, order, snake_item(k)).cn;
     total = __reduce_add_sync(0xFFFFFFFFu, total);
-    auto ready = [](uint64_t* bar, int phase) {
-      return __all_sync(0xFFFFFFFFu, mbar_test_wait(bar, phase & 1)) != 0;
-    };
-    int ts = 0, tu = 0, to = 0, tp = 0;  // next chunk of each stream
+    // Seven lanes hold one barrier each that the streams' next products wait for, so that one
+    // test answers for all of them (one after another the tests took as long as the products).
+    // A barrier that frees a buffer starts at parity 1, as if its first phase had passed; P V has
+    // one buffer, so that it waits for the outputs of the chunk before, in the other barrier.
+    enum { kP, kPe, kR, kOe, kVf, kUe, kQk, kTests };
+    uint64_t* const base[kTests] = {p_full, o_empty, r_full, o_empty, vp_full, u_empty, qk_full};
+    constexpr int kLen[kTests] = {2, 2, 1, 2, NU, NU, ST};
+    uint64_t* mine = p_full;
+    int ring = 1;
+#pragma unroll
+    for (int x = 0; x < kTests; ++x)
+      if (lane == x) mine = base[x], ring = kLen[x];
+    int at = lane == kPe || (lane == kOe && L::kNo == 1);
+    uint32_t parity = lane == kPe || lane == kOe || lane == kUe;
+    const uint32_t stream = lane <= kPe ? 1u : lane <= kOe ? 2u : lane <= kUe || !OUT ? 4u : 8u;
+    int ts = 0, tu = 0, to = 0, tp = 0, idle = 0;  // next chunk of each stream
     long long t0 = clock64();
     const long long limit = static_cast<long long>(p.wait_ns) * 2;
     while ((OUT ? tp : tu) < total) {
-      bool progress = false;
-      if (OUT && tp < to && ready(p_full + (tp & 1), tp >> 1)) {
+      const uint32_t ready = __ballot_sync(0xFFFFFFFFu, mbar_test_wait(mine + at, parity));
+      __syncwarp();  // what one lane's test has seen the issuing lane sees
+      tc_fence_after();
+      uint32_t issued = 0u;
+      if (OUT && tp < to && (~ready & (1u << kP | 1u << kPe)) == 0u) {
         // O2 = P V (P from TMEM)
-        tc_fence_after();
         const uint32_t v_base = smem_u32(smem + L::kV + (tp % VS) * L::kBox);
         mma_pv8_commit_w(tmem + L::kTO2, tmem + L::kTS + (tp & 1) * 128,
                          sw128_desc_lo(v_base, L::kBox), kHi, idesc_o, 0u, pv_done + tp % VS);
         ++tp;
-        progress = true;
+        issued |= 1u;
       }
-      if (OUT && to < tu && ready(r_full, to) && (to == 0 || ready(o_empty, to - 1))) {
+      if (OUT && to < tu && (~ready & (1u << kR | 1u << kOe)) == 0u) {
         // O1 = Q R; with S and U of the chunk issued before, Q and K are free after it
-        tc_fence_after();
         const uint32_t q_base = smem_u32(smem + L::kQ + (to % ST) * L::kTile);
         const uint32_t r_base = smem_u32(smem + L::kR);
-        mma_qr_commit_w<D / 16>(tmem + L::kTO1, sw128_desc_lo(q_base, 16),
+        mma_qr_commit_w<D / 16>(tmem + L::kTO1 + to % L::kNo * kCols, sw128_desc_lo(q_base, 16),
                                 sw128_desc_lo(r_base, L::kBox), kHi, idesc_o,
                                 qk_empty + to % ST);
         ++to;
-        progress = true;
+        issued |= 2u;
       }
-      if (tu < (OUT ? ts : total) && ready(vp_full + tu % NU, tu / NU) &&
-          (tu < NU || ready(u_empty + tu % NU, tu / NU - 1)) &&
-          (OUT || ready(qk_full + tu % ST, tu / ST))) {
+      if (tu < (OUT ? ts : total) &&
+          (~ready & (1u << kVf | 1u << kUe | (OUT ? 0u : 1u << kQk))) == 0u) {
         // U = K^T (V' | its rounding error).  A holds the K columns as rows: 128 for d = 128;
         // for d = 64 the chunk stride of 0 gives them twice, lanes 64-127 a copy of 0-63.
-        tc_fence_after();
         const uint32_t k_base = smem_u32(smem + L::kK + (tu % ST) * L::kTile);
         const uint32_t v_base = smem_u32(smem + L::kVp + tu % NU * L::kVpSize);
         mma_kv_commit_w(tmem + (tu % NU == 0 ? L::kTU : L::kTS),
@@ -475,21 +500,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_w(pv_done + tu % VS);
         }
         ++tu;
-        progress = true;
+        issued |= 4u;
       }
-      if (OUT && ts < total && ts < tp + 2 && ready(qk_full + ts % ST, ts / ST)) {
+      if (OUT && ts < total && ts < tp + 2 && (ready >> kQk & 1u)) {
         // S = Q K^T
-        tc_fence_after();
         const uint32_t q_base = smem_u32(smem + L::kQ + (ts % ST) * L::kTile);
         const uint32_t k_base = smem_u32(smem + L::kK + (ts % ST) * L::kTile);
         mma_s_commit_w<D / 16>(tmem + L::kTS + (ts & 1) * 128, sw128_desc_lo(q_base, 16),
                                sw128_desc_lo(k_base, 16), kHi, idesc_s, s_full + (ts & 1));
         ++ts;
-        progress = true;
+        issued |= 8u;
       }
-      if (progress) {
+      if (issued & stream) {
+        at = at + 1 == ring ? 0 : at + 1;
+        parity ^= at == 0;
+      }
+      if (issued) {
+        idle = 0;
+      } else if (++idle == 1) {
         t0 = clock64();
-      } else {
+      } else if (idle % 32 == 0) {
         const bool late = __any_sync(0xFFFFFFFFu, clock64() - t0 > limit);
         if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) {
           if (lane == 0 && late) atomicOr(p.status, kStatusTimeout);
@@ -521,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && take(k, it); ++k) {
         const bool rev = p.pass[it.pass].reverse != 0;
         const float l2 = it.l2;
+        const int steep = l2 < -2.0f;  // see weigh
         __syncwarp();
         pow[lane] = ex2_approx(l2 * static_cast<float>(rev ? lane : 31 - lane));
         __syncwarp();
@@ -530,35 +561,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = mbar_wait_w(s_full + (t & 1), (t >> 1) & 1, wctx))) break;
           tc_fence_after();
           // P of keys c0.. goes to column (c0 / 64) 64 + (c0 % 64) / 2, where S has been read
-          // by then.
+          // by then.  Blocks [b0, b1) are weighed, 16 columns while the next 16 are read.
+          const int b0 = rev ? wq + steep : 0, b1 = rev ? 4 : wq + 1 - steep;
+          uint32_t sa[16], se[16], pk[8];
+          const auto near = [&] {
 #pragma unroll 1
-          for (int blk = 0; blk < 4; ++blk) {
+            for (int c0 = 0; c0 < 32; c0 += 16) {
+              tmem_ld16(sb + wq * 32 + c0, sa);
+              tmem_wait_ld();
+              weigh_near(sa, l2, rev, c0 - lane, m - wq * 32 - c0, pk);
+              tmem_st8(sb + (wq & 2) * 32 + (wq & 1) * 16 + c0 / 2, pk);
+            }
+          };
+          if (steep && rev) near();
+          if (b0 < b1) tmem_ld16(sb + b0 * 32, sa);
+#pragma unroll 1
+          for (int blk = b0; blk < b1; ++blk) {
             const uint32_t src = sb + blk * 32, dst = sb + (blk & 2) * 32 + (blk & 1) * 16;
             const int last = m - blk * 32;
-            if (blk == wq) {
-#pragma unroll 1
-              for (int c0 = 0; c0 < 32; c0 += 16) {
-                uint32_t sr[16], pk[8];
-                tmem_ld16(src + c0, sr);
-                tmem_wait_ld();
-                weigh_near(sr, l2, rev, c0 - lane, last - c0, pk);
-                tmem_st8(dst + c0 / 2, pk);
-              }
-            } else {
-              uint32_t pk[16];
-              if (rev ? blk < wq : blk > wq) {
+            const bool masked = blk == wq || last < 32;
+            uint32_t keep = blk != wq ? ~0u : rev ? ~0u << lane : ~0u >> (31 - lane);
+            if (last < 32) keep &= last <= 0 ? 0u : (1u << last) - 1u;
+            const float f =
+                ex2_approx(l2 * static_cast<float>(rev ? blk * 32 - i : i - blk * 32 - 31));
+            tmem_wait_ld_of(sa);
+            tmem_ld16(src + 16, se);
+            weigh(sa, f, pow, masked, keep, pk);
+            tmem_st8(dst, pk);
+            tmem_wait_ld_of(se);
+            if (blk + 1 < b1) tmem_ld16(src + 32, sa);
+            weigh(se, f, pow + 16, masked, keep >> 16, pk);
+            tmem_st8(dst + 8, pk);
+          }
+          if (steep && !rev) near();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) pk[c] = 0u;
-              } else {
-                uint32_t sr[32];
-                tmem_ld32(src, sr);
-                tmem_wait_ld();
-                const float f = ex2_approx(
-                    l2 * static_cast<float>(rev ? blk * 32 - i : i - blk * 32 - 31));
-                weigh_far(sr, f, pow, last, pk);
-              }
-              tmem_st16(dst, pk);
-            }
+          for (int c = 0; c < 8; ++c) pk[c] = 0u;
+#pragma unroll 1
+          for (int blk = rev ? 0 : wq + 1; blk < (rev ? wq : 4); ++blk) {
+            tmem_st8(sb + (blk & 2) * 32 + (blk & 1) * 16, pk);
+            tmem_st8(sb + (blk & 2) * 32 + (blk & 1) * 16 + 8, pk);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -661,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
             uint32_t a[16], b[16], pk[8];
-            tmem_ld16(t_lane + L::kTO1 + x * 16, a);
+            tmem_ld16(t_lane + L::kTO1 + t % L::kNo * kCols + x * 16, a);
             tmem_ld16(t_lane + L::kTO2 + x * 16, b);
             tmem_wait_ld();
 #pragma unroll
@@ -680,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(o_empty);
+          if (lane == 0) mbar_arrive(o_empty + (t & 1));
           const int row = c * kChunk + wq * 32;  // of the sequence
           if (!p.cu || wq * 32 + 32 <= m) {
             // padded: rows behind the sequence are 0, rows behind the tensor not written

@@ -126,6 +126,15 @@ def test_decays(g, d):
     _check(t, torch.tensor([g, -0.1]), [260, 133], False, 260)
 
 
+@pytest.mark.parametrize("g", [-1.38, -1.39])  # lambda a little above and below 1/4
+def test_large_scores_and_steep_decays(g):
+    """Scores of 2^66 and more against weights down to lambda^127: no product overflows on its
+    way to a finite output."""
+    t = _make((1, 300), 1, 64, 1, False, seed=30)
+    t["q"], t["k"] = t["q"] * 2.0 ** 32, t["k"] * 2.0 ** 32
+    _check(t, torch.full((1,), g), [300], False, 300, scale=2.0 ** -64)
+
+
 @pytest.mark.parametrize("scale", [1.0, -0.5, 0.0])
 def test_scales(scale):
     t = _make((1, 150), 1, 64, 1, True, seed=6)
