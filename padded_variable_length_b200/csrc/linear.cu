@@ -23,7 +23,7 @@
 // 128 bytes a cycle and waiting.  For a chunk of d = 128 (64 of the value columns) 80 KB come
 // in, the products fetch 64 (S), 16 (P V), 48 (Q R) and 48 KB (K^T V'; 64 with a V' of two
 // numbers), V' takes 32 (48), R 16 and the outputs 32: 2690 cycles (2940).  The long ragged batch
-// (8 x 4096..16384, 16 heads of 128), 153 chunks on the fullest SM, takes 292 us, 3600 cycles
+// (8 x 4096..16384, 16 heads of 128), 153 chunks on the fullest SM, takes 287 us, 3600 cycles
 // each; the copy of its tensors 233.  The rest is a chunk's jobs that wait for one another, and
 // its loads for the products that free their stage: with Q R in two buffers, so that it need not
 // wait for the outputs of the chunk before, and the issuer's tests side by side, that batch went
@@ -436,7 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- MMA issuer
     // Four streams of products, each in chunk order; whichever has its operands goes next.
     // The tensor pipe runs in issue order, so a buffer may be overwritten by a product that
-    // is issued after the last one that reads it.
+    // is issued after the last one that reads it.  A test after a product waits some 500 cycles
+    // behind it, so U comes before Q R, which may then follow it at once (287 us; the other way
+    // round 292 on the long ragged batch).
     constexpr uint32_t kHi = sw128_desc_hi(1024);
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(128, kCols, true);
@@ -476,16 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tp;
         issued |= 1u;
       }
-      if (OUT && to < tu && (~ready & (1u << kR | 1u << kOe)) == 0u) {
-        // O1 = Q R; with S and U of the chunk issued before, Q and K are free after it
-        const uint32_t q_base = smem_u32(smem + L::kQ + (to % ST) * L::kTile);
-        const uint32_t r_base = smem_u32(smem + L::kR);
-        mma_qr_commit_w<D / 16>(tmem + L::kTO1 + to % L::kNo * kCols, sw128_desc_lo(q_base, 16),
-                                sw128_desc_lo(r_base, L::kBox), kHi, idesc_o,
-                                qk_empty + to % ST);
-        ++to;
-        issued |= 2u;
-      }
       if (tu < (OUT ? ts : total) &&
           (~ready & (1u << kVf | 1u << kUe | (OUT ? 0u : 1u << kQk))) == 0u) {
         // U = K^T (V' | its rounding error).  A holds the K columns as rows: 128 for d = 128;
@@ -501,6 +493,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++tu;
         issued |= 4u;
+      }
+      if (OUT && to < tu && (~ready & (1u << kR | 1u << kOe)) == 0u) {
+        // O1 = Q R; with S and U of the chunk issued before, Q and K are free after it
+        const uint32_t q_base = smem_u32(smem + L::kQ + (to % ST) * L::kTile);
+        const uint32_t r_base = smem_u32(smem + L::kR);
+        mma_qr_commit_w<D / 16>(tmem + L::kTO1 + to % L::kNo * kCols, sw128_desc_lo(q_base, 16),
+                                sw128_desc_lo(r_base, L::kBox), kHi, idesc_o,
+                                qk_empty + to % ST);
+        ++to;
+        issued |= 2u;
       }
       if (OUT && ts < total && ts < tp + 2 && (ready >> kQk & 1u)) {
         // S = Q K^T
