@@ -19,15 +19,15 @@
 //   o_i = lambda^r R^T q_i + sum_{j >= i} lambda^(j-i) (..),  R <- lambda^m R + sum_j lambda^(j+1) k_j v_j^T
 //
 // What it has to move: q, k, v and o once (the backward seven tensors; its passes read ten, the
-// two that run side by side sharing their reads through L2).  What bounds it is shared memory's
-// 128 bytes a cycle and waiting.  For a chunk of d = 128 (64 of the value columns) 80 KB come
-// in, the products fetch 64 (S), 16 (P V), 48 (Q R) and 48 KB (K^T V'; 64 with a V' of two
-// numbers), V' takes 32 (48), R 16 and the outputs 32: 2690 cycles (2940).  The long ragged batch
-// (8 x 4096..16384, 16 heads of 128), 153 chunks on the fullest SM, takes 287 us, 3600 cycles
-// each; the copy of its tensors 233.  The rest is a chunk's jobs that wait for one another, and
-// its loads for the products that free their stage: with Q R in two buffers, so that it need not
-// wait for the outputs of the chunk before, and the issuer's tests side by side, that batch went
-// from 303 to 292 us and the gradients of the documents below from 335 to 316.
+// two that run side by side sharing their reads through L2).  What bounds it is waiting: with full
+// lengths (16 x 2048, 16 heads of 128) DRAM is 53 % busy, the tensor pipe 36 %, shared memory's
+// banks 24 % (reads) and 14 % (writes), the issue slots 50 %.  A chunk's jobs hang on each other
+// (the weights of a warp whose rows see all keys take 2300 of a chunk's 3600 cycles), and its
+// loads, 2200 to 5600 cycles, on the products that free their stage.  With Q R in two buffers, so
+// that it need not wait for the outputs of the chunk before, and the issuer's tests side by side,
+// the long ragged batch (8 x 4096..16384, 16 heads of 128) went from 303 to 292 us and the
+// gradients of the documents below from 335 to 316; 287 us is 3500 cycles a chunk on the SM with
+// the most, 153, and the copy of its tensors 233.
 // Layout: 128 tokens a chunk are the M of every product; d = 128 is cut into two items of 64
 // value columns, because all of its operands fit shared memory twice that way (one item of 128
 // columns leaves K and Q single stages, whose copies nothing hides: 553 us).
