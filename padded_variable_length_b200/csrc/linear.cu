@@ -425,12 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
     if (lane == 0) {
-      if (*abort_flag) {
-        // Let the copies still in flight land before the CTA's shared memory goes away.
-        const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
-        for (int u = max(0, t - ST); u < t; ++u) mbar_wait(qk_full + u % ST, (u / ST) & 1, drain);
-        for (int u = max(0, tv - VS); u < tv; ++u) mbar_wait(v_full + u % VS, (u / VS) & 1, drain);
-      }
+      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
+      // the warps that wait for them may give up after this one has issued its last.
+      const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
+      for (int u = max(0, t - ST); u < t; ++u) mbar_wait(qk_full + u % ST, (u / ST) & 1, drain);
+      for (int u = max(0, tv - VS); u < tv; ++u) mbar_wait(v_full + u % VS, (u / VS) & 1, drain);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -534,13 +533,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(done);
     const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
     mbar_wait_w(done, 0, drain);
-    // ... and every commit's arrival seen: nobody else waits for the last ones of these, and
-    // none may come when the CTA's shared memory is another's
+    // ... and every commit's arrival seen, as none may come when the CTA's shared memory is
+    // another's: nobody else waits for the last ones of qk_empty and pv_done, and after an abort
+    // the warps that would have waited for s_full and u_full are gone
     const int nqk = OUT ? to : tu, npv = OUT ? tp : tu;
     for (int u = max(0, nqk - ST); u < nqk; ++u)
       mbar_wait_w(qk_empty + u % ST, (u / ST) & 1, drain);
     for (int u = max(0, npv - VS); u < npv; ++u)
       mbar_wait_w(pv_done + u % VS, (u / VS) & 1, drain);
+    for (int u = max(0, ts - 2); u < ts; ++u) mbar_wait_w(s_full + (u & 1), (u >> 1) & 1, drain);
+    for (int u = max(0, tu - NU); u < tu; ++u)
+      mbar_wait_w(u_full + u % NU, (u / NU) & 1, drain);
   } else if (warp < kWarpV) {
     // ---------------------------------------------------------------- P = decayed, masked S
     if (OUT) {
