@@ -430,7 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
+    if (lane == 0) {
+      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
+      // the warps that wait for them may give up after this one has issued its last.
       const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
       for (int u = max(0, ii - KVB); u < ii; ++u) mbar_wait(kv_full + u % KVB, (u / KVB) & 1, drain);
       for (int u = max(0, qc - S); u < qc; ++u) mbar_wait(q_full + u % S, (u / S) & 1, drain);
@@ -977,7 +979,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
+    if (lane == 0) {
+      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
+      // the warps that wait for them may give up after this one has issued its last.
       const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
       for (int u = max(0, ii - QB); u < ii; ++u) mbar_wait(qd_full + u % QB, (u / QB) & 1, drain);
       for (int u = max(0, tk_ - S); u < tk_; ++u) mbar_wait(kv_full + u % S, (u / S) & 1, drain);
@@ -1560,8 +1564,9 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // Let the copies still in flight land before the CTA's shared memory goes away.
+    if (lane == 0) {
+      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
+      // the warps that wait for them may give up after this one has issued its last.
       const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
       for (int u = max(0, ii - 2); u < ii; ++u) mbar_wait(kv_full + (u & 1), (u >> 1) & 1, drain);
       for (int u = max(0, qc - S); u < qc; ++u) mbar_wait(q_full + u % S, (u / S) & 1, drain);

@@ -283,8 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0 && *abort_flag) {
-      // Let the copies still in flight land before the CTA's shared memory goes away.
+    if (lane == 0) {
+      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
+      // the warps that wait for them may give up after this one has issued its last.
       const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
       for (int u = max(0, i - 2); u < i; ++u) mbar_wait(q_full + (u & 1), (u >> 1) & 1, drain);
       for (int u = max(0, t - S); u < t; ++u) {
@@ -763,8 +764,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok)
       while (zeroing && zw < p.nitems) zero_one();
     if (zeroing) bulk_wait_all();  // the stores have read the box before shared memory goes
-    if (lane == 0 && *abort_flag) {
-      // Let the copies still in flight land before the CTA's shared memory goes away.
+    if (lane == 0) {
+      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
+      // the warps that wait for them may give up after this one has issued its last.
       const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
       if (role == 0)
         for (int u = max(0, i - 2); u < i; ++u) mbar_wait(q_full + (u & 1), (u >> 1) & 1, drain);
