@@ -520,20 +520,44 @@ def _out(t: Optional[torch.Tensor], like: torch.Tensor, like_lay: _Layout, name:
     return t, lay
 
 
-def _workspace(workspace, need: int, like: torch.Tensor, dev: int, stream):
-    """(tensor, pointer, bytes): the caller's buffer, or a new one of `need` bytes, which must
-    not be handed out again before the call has run on a stream other than the current one."""
+def _workspace(workspace, need: int, like: torch.Tensor, dev: int):
+    """(tensor, pointer, bytes): the caller's buffer, or a new one of `need` bytes."""
     if workspace is None:
         if need == 0:
             return None, None, 0
         workspace = like.new_empty(need, dtype=torch.uint8)
-        if stream is not None:
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                    torch.cuda.ExternalStream(_stream(stream)))
         return workspace, workspace.data_ptr(), need
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the current CUDA device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _in_order(call):
+    """A call that is given a stream runs with that stream as torch's current one: what it
+    allocates, zeroes or copies is then in the stream's order, as its kernels are, and not beside
+    work of the current stream that still uses the same memory.  The caller's tensors are kept
+    until the stream has run the call, and new ones until the current stream has used them."""
+    at = call.__code__.co_varnames[:call.__code__.co_argcount].index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream(stream)  # 0 and 1 are names of the default stream
+            stream = torch.cuda.ExternalStream(handle) if handle not in (None, 0, 1) else torch.cuda.default_stream()
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            got = call(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, _Tensor) and t.is_cuda:
+                t.record_stream(stream)
+        for t in got if isinstance(got, tuple) else (got,):
+            if t is not None:
+                t.record_stream(here)
+        return got
+    return run
 
 
 def _qk_shape(qs, ks):
@@ -601,6 +625,7 @@ def _pair(t, lay):
     return (None, _NO_STRIDES) if t is None else (t.data_ptr(), lay.strides)
 
 
+@_in_order
 def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None, sections=None,
                  interleaved: bool = False, lengths=None, norm: bool = True, out_q=None, out_k=None, stream=None):
     """(yq, yk): every head of q and k normed by its root mean square (norm=False: not),
@@ -625,6 +650,7 @@ def qk_norm_rope_bwd_workspace_bytes(B: int, N: int, d: int) -> int:
     return n.value
 
 
+@_in_order
 def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None,
                      sections=None, interleaved: bool = False, lengths=None, norm: bool = True, dq=None, dk=None,
                      workspace=None, stream=None):
@@ -653,7 +679,7 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
     if not (head[0] and head[1] and head[2] + head[3]):
         return outs[0], outs[1], *(None if g is None else g.zero_() for g in grads)
     need = qk_norm_rope_bwd_workspace_bytes(head[0], head[1], head[4]) if gq is not None or gk is not None else 0
-    ws, wp, wn = _workspace(workspace, need, q if q is not None else k, dev, stream)
+    ws, wp, wn = _workspace(workspace, need, q if q is not None else k, dev)
     _check(_lib.sigattn_qk_norm_rope_bwd(*head, *_pair(q, ql), *_pair(k, kl), *args[0][:2], *args[1][:2], *rot,
                                          *args[0][2:], *args[1][2:], None if gq is None else gq.data_ptr(),
                                          None if gk is None else gk.data_ptr(), wp, wn, _stream(stream)),
@@ -706,6 +732,7 @@ def _hand_on(to: Optional[torch.Tensor], state: Optional[torch.Tensor]):
     return to
 
 
+@_in_order
 def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None,
                return_state: bool = False, scale: Optional[float] = None, out=None, final_state=None,
                workspace=None, stream=None):
@@ -726,12 +753,13 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
         fp = final_state.data_ptr()
     if N == 0 or q.numel() == 0:
         return out, _hand_on(final_state, state)
-    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev, stream)
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev)
     _check(_lib.sigattn_linear_fwd(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, wp, wn, _stream(stream)),
            "linear_fwd")
     return out, final_state
 
 
+@_in_order
 def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None, dstate=None,
                scale: Optional[float] = None, dq=None, dk=None, dv=None, dstate_out=None, workspace=None, stream=None):
     """(dq, dk, dv, dstate_out): gradients of linear_fwd from do and, for a loss that uses the
@@ -750,12 +778,13 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
         gp = dstate_out.data_ptr()
     if N == 0 or q.numel() == 0:
         return dq, dk, dv, _hand_on(dstate_out, dstate)
-    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev, stream)
+    ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev)
     _check(_lib.sigattn_linear_bwd(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,
                                    dv.data_ptr(), dvl.strides, gp, wp, wn, _stream(stream)), "linear_bwd")
     return dq, dk, dv, dstate_out
 
 
+@_in_order
 def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] = None, state_out=None, out=None,
                 stream=None) -> torch.Tensor:
     """o of one token of each sequence, q, k, v bf16 [B, H, d]; ``state`` fp32 [B, H, d, d] is
