@@ -447,7 +447,9 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * [0, N]; NULL: all N) and its pad rows come out as exactly 0, whatever they hold (NaN
  * included).  With cu_seqlens (device int32 [B + 1], non-decreasing; lengths must be NULL),
  * packed [T, H, d] tensors, sequence b in rows cu_seqlens[b] .. cu_seqlens[b + 1]; N is the
- * longest sequence (a longer one is cut there) and rows of no sequence are not written.
+ * longest sequence (a longer one is cut there) and rows of no sequence are not written; the
+ * calls that end in _ex write them as 0 in the outputs that zero_rest names (bit 0: o, or bits
+ * 0, 1, 2: dq, dk, dv).
  * Pointers, strides and d (64, 128) as above; states and workspace 16-byte aligned.  Outputs
  * must not overlap inputs or one another (the very same pointer is refused); an input's heads
  * or tokens may share memory (stride 0), and each of them then has a gradient of its own.
@@ -467,8 +469,8 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  * dstate must not overlap state or dfinal_state.  log_decay has no gradient.
  *
  * Errors: INVALID (null pointer, B, N, H or T < 1, both lengths and cu_seqlens, non-finite
- * scale, workspace missing or too small, states that overlap where they must not, an output
- * that is an input), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT, NO_DEVICE, CUDA; TIMEOUT
+ * scale, zero_rest of other bits, workspace missing or too small, states that overlap where
+ * they must not, an output that is an input), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT, NO_DEVICE, CUDA; TIMEOUT
  * through sigattn_get_status.
  */
 SIGATTN_API int sigattn_linear_workspace_size(int B, int N, int H, int d, int backward,
@@ -493,6 +495,26 @@ SIGATTN_API int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const 
                                    void* dv, const int64_t dv_strides[3],
                                    float* dstate, void* workspace, size_t workspace_bytes,
                                    sigattn_stream stream);
+SIGATTN_API int sigattn_linear_fwd_ex(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                      const int32_t* cu_seqlens, const float* log_decay,
+                                      float scale, const void* q, const int64_t q_strides[3],
+                                      const void* k, const int64_t k_strides[3],
+                                      const void* v, const int64_t v_strides[3],
+                                      const float* state, void* o, const int64_t o_strides[3],
+                                      float* final_state, int zero_rest, void* workspace,
+                                      size_t workspace_bytes, sigattn_stream stream);
+SIGATTN_API int sigattn_linear_bwd_ex(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                      const int32_t* cu_seqlens, const float* log_decay,
+                                      float scale, const void* q, const int64_t q_strides[3],
+                                      const void* k, const int64_t k_strides[3],
+                                      const void* v, const int64_t v_strides[3],
+                                      const void* dout, const int64_t do_strides[3],
+                                      const float* state, const float* dfinal_state,
+                                      void* dq, const int64_t dq_strides[3],
+                                      void* dk, const int64_t dk_strides[3],
+                                      void* dv, const int64_t dv_strides[3],
+                                      float* dstate, int zero_rest, void* workspace,
+                                      size_t workspace_bytes, sigattn_stream stream);
 
 /*
  * One token of each sequence: q, k, v, o bf16 with d contiguous and {batch, head} strides

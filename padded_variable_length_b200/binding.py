@@ -100,6 +100,10 @@ _sig("sigattn_linear_fwd", ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, ctype
      ctypes.c_float, *[_p, _I64x3] * 3, _p, _p, _I64x3, _p, _p, ctypes.c_size_t, _p)
 _sig("sigattn_linear_bwd", ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, _p, _p, _p,
      ctypes.c_float, *[_p, _I64x3] * 4, _p, _p, *[_p, _I64x3] * 3, _p, _p, ctypes.c_size_t, _p)
+_sig("sigattn_linear_fwd_ex", ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, _p, _p, _p,
+     ctypes.c_float, *[_p, _I64x3] * 3, _p, _p, _I64x3, _p, ctypes.c_int, _p, ctypes.c_size_t, _p)
+_sig("sigattn_linear_bwd_ex", ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, _p, _p, _p,
+     ctypes.c_float, *[_p, _I64x3] * 4, _p, _p, *[_p, _I64x3] * 3, _p, ctypes.c_int, _p, ctypes.c_size_t, _p)
 _sig("sigattn_linear_step", ctypes.c_int, *[ctypes.c_int] * 3, _p, _p, ctypes.c_float, *[_p, _I64x2] * 3, _p, _p,
      _p, _I64x2, _p)
 _sig("sigattn_get_status", ctypes.c_int, _p)
@@ -740,22 +744,24 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
     k v^T, o = scale S^T q for each token in turn.  q, k, v bf16 [B, N, H, d] (with lengths) or
     packed [T, H, d] (with cu_seqlens and max_seqlen); state fp32 [B, H, d, d] is what the
     sequences start from (None: 0).  The final state is returned where return_state is set or
-    a buffer for it is given, else None."""
+    a buffer for it is given, else None.  Rows of no sequence come out as 0; of a packed tensor
+    given as ``out`` they stay as they are."""
     dev = _here()
     head, (sp, fp), pairs, lay = _linear_args(q, ((k, "k"), (v, "v")), log_decay, lengths, cu_seqlens, max_seqlen,
                                               ((state, "state"), (final_state, "final_state")), dev)
     B, N, _, H, d = head[:5]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    rest = 1 if out is None else 0
     out, ol = _out(out, q, lay, "out", dev)
     if return_state and final_state is None:
         final_state = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
         fp = final_state.data_ptr()
     if N == 0 or q.numel() == 0:
-        return out, _hand_on(final_state, state)
+        return out.zero_() if rest else out, _hand_on(final_state, state)
     ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev)
-    _check(_lib.sigattn_linear_fwd(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, wp, wn, _stream(stream)),
-           "linear_fwd")
+    _check(_lib.sigattn_linear_fwd_ex(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, rest, wp, wn,
+                                      _stream(stream)), "linear_fwd")
     return out, final_state
 
 
@@ -764,7 +770,7 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
                scale: Optional[float] = None, dq=None, dk=None, dv=None, dstate_out=None, workspace=None, stream=None):
     """(dq, dk, dv, dstate_out): gradients of linear_fwd from do and, for a loss that uses the
     final state, its gradient ``dstate``.  dstate_out, the gradient of ``state``, is None where
-    there was no state (unless a buffer for it is given)."""
+    there was no state (unless a buffer for it is given).  Rows of no sequence as in linear_fwd."""
     dev = _here()
     head, (sp, ep, gp), pairs, lay = _linear_args(
         q, ((k, "k"), (v, "v"), (do, "do")), log_decay, lengths, cu_seqlens, max_seqlen,
@@ -772,15 +778,16 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
     B, N, _, H, d = head[:5]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
+    rest = sum(1 << i for i, t in enumerate((dq, dk, dv)) if t is None)
     (dq, dql), (dk, dkl), (dv, dvl) = _out(dq, q, lay, "dq", dev), _out(dk, k, lay, "dk", dev), _out(dv, v, lay, "dv", dev)
     if state is not None and dstate_out is None:
         dstate_out = torch.empty_like(state)
         gp = dstate_out.data_ptr()
     if N == 0 or q.numel() == 0:
-        return dq, dk, dv, _hand_on(dstate_out, dstate)
+        return *(t.zero_() if rest >> i & 1 else t for i, t in enumerate((dq, dk, dv))), _hand_on(dstate_out, dstate)
     ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev)
-    _check(_lib.sigattn_linear_bwd(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,
-                                   dv.data_ptr(), dvl.strides, gp, wp, wn, _stream(stream)), "linear_bwd")
+    _check(_lib.sigattn_linear_bwd_ex(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,
+                                      dv.data_ptr(), dvl.strides, gp, rest, wp, wn, _stream(stream)), "linear_bwd")
     return dq, dk, dv, dstate_out
 
 

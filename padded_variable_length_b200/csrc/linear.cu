@@ -70,6 +70,7 @@ struct LinPass {
   int init_sr, init_sc;  // (b, h) at (b H + h) D D + row init_sr + col init_sc
   float* fin;            // state after the last chunk [B, H, D, D], nullptr: not wanted
   float* seg;            // [B, H, nseg, D, D]: see sigattn_linear_workspace_size
+  int rest;              // packed: rows of no sequence are written as 0
 };
 
 struct LinParams {
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, OUT ? (p.cu ? 21 : 22) : 17);  // the warps that take items
+      mbar_init(item_empty + i, OUT ? 22 : 17);  // the warps that take items
     }
     *abort_flag = 0;
     *drain_flag = 0;
@@ -833,15 +834,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpI + 1) {
     // ---------------------------------------------------------------- zero rows
     // Rows behind a padded sequence's last chunk, within the item's segment, are written as 0
-    // (those inside it come out of the chunk as 0).
-    if (OUT && !p.cu) {
+    // (those inside it come out of the chunk as 0); where asked, so are packed rows of no
+    // sequence, those from a sequence's end to the next one's start by its segments in equal
+    // parts, those before the first by the first's.
+    if (OUT) {
       Item it;
       for (int k = 0; take(k, it); ++k) {
         const LinPass& ps = p.pass[it.pass];
-        const int lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk);
-        const int hi = it.seg == p.nseg - 1 ? p.N : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
-        __nv_bfloat16* out =
-            ps.out + it.b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols + lane % 8 * 8;
+        __nv_bfloat16* out = ps.out + it.s.tma_b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols +
+                             lane % 8 * 8;
+        int lo, hi;
+        if (!p.cu) {
+          lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk);
+          hi = it.seg == p.nseg - 1 ? p.N : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
+        } else if (ps.rest) {
+          lo = it.s.row0 + it.s.n;
+          hi = it.b + 1 < p.B ? max(lo, min(__ldg(p.cu + it.b + 1), p.T)) : p.T;
+          const int part = (hi - lo + p.nseg - 1) / p.nseg;
+          lo += it.seg * part;
+          hi = min(hi, lo + part);
+          if (it.b == 0 && it.seg == 0)
+            for (int r = lane / 8; r < it.s.row0; r += 4)
+              *reinterpret_cast<uint4*>(out + r * ps.o_sn) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+          continue;
+        }
         for (int r = lo + lane / 8; r < hi; r += 4)
           *reinterpret_cast<uint4*>(out + r * ps.o_sn) = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -1131,9 +1148,22 @@ extern "C" int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const i
                                   const int64_t v_strides[3], const float* state, void* o,
                                   const int64_t o_strides[3], float* final_state, void* workspace,
                                   size_t workspace_bytes, sigattn_stream s) {
+  return sigattn_linear_fwd_ex(B, N, T, H, d, lengths, cu_seqlens, log_decay, scale, q, q_strides, k,
+                               k_strides, v, v_strides, state, o, o_strides, final_state, 0,
+                               workspace, workspace_bytes, s);
+}
+
+extern "C" int sigattn_linear_fwd_ex(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                     const int32_t* cu_seqlens, const float* log_decay,
+                                     float scale, const void* q, const int64_t q_strides[3],
+                                     const void* k, const int64_t k_strides[3], const void* v,
+                                     const int64_t v_strides[3], const float* state, void* o,
+                                     const int64_t o_strides[3], float* final_state, int zero_rest,
+                                     void* workspace, size_t workspace_bytes, sigattn_stream s) {
   const bool packed = cu_seqlens != nullptr;
   int rc = check_sizes(B, N, T, H, d, packed);
   if (rc != SIGATTN_OK) return rc;
+  if (zero_rest & ~1) return SIGATTN_ERR_INVALID;
   if (!log_decay || !std::isfinite(scale) || (packed && lengths)) return SIGATTN_ERR_INVALID;
   const int rows = packed ? static_cast<int>(T) : N;
   TensorDesc t[3], to;
@@ -1163,6 +1193,7 @@ extern "C" int sigattn_linear_fwd(int B, int N, int64_t T, int H, int d, const i
   ps.init_sc = 1;
   ps.fin = final_state;
   ps.seg = static_cast<float*>(workspace);
+  ps.rest = zero_rest;
   const cudaStream_t stream = static_cast<cudaStream_t>(s);
   return d == 64 ? launch<64>(p, stream) : launch<128>(p, stream);
 }
@@ -1177,9 +1208,27 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
                                   void* dk, const int64_t dk_strides[3], void* dv,
                                   const int64_t dv_strides[3], float* dstate, void* workspace,
                                   size_t workspace_bytes, sigattn_stream s) {
+  return sigattn_linear_bwd_ex(B, N, T, H, d, lengths, cu_seqlens, log_decay, scale, q, q_strides, k,
+                               k_strides, v, v_strides, dout, do_strides, state, dfinal_state, dq,
+                               dq_strides, dk, dk_strides, dv, dv_strides, dstate, 0, workspace,
+                               workspace_bytes, s);
+}
+
+extern "C" int sigattn_linear_bwd_ex(int B, int N, int64_t T, int H, int d, const int32_t* lengths,
+                                     const int32_t* cu_seqlens, const float* log_decay,
+                                     float scale, const void* q, const int64_t q_strides[3],
+                                     const void* k, const int64_t k_strides[3], const void* v,
+                                     const int64_t v_strides[3], const void* dout,
+                                     const int64_t do_strides[3], const float* state,
+                                     const float* dfinal_state, void* dq,
+                                     const int64_t dq_strides[3], void* dk,
+                                     const int64_t dk_strides[3], void* dv,
+                                     const int64_t dv_strides[3], float* dstate, int zero_rest,
+                                     void* workspace, size_t workspace_bytes, sigattn_stream s) {
   const bool packed = cu_seqlens != nullptr;
   int rc = check_sizes(B, N, T, H, d, packed);
   if (rc != SIGATTN_OK) return rc;
+  if (zero_rest & ~7) return SIGATTN_ERR_INVALID;
   if (!log_decay || !std::isfinite(scale) || (packed && lengths)) return SIGATTN_ERR_INVALID;
   const int rows = packed ? static_cast<int>(T) : N;
   TensorDesc t[4], out[3];
@@ -1206,8 +1255,10 @@ extern "C" int sigattn_linear_bwd(int B, int N, int64_t T, int H, int d, const i
       SIGATTN_OK)
     return rc;
   const size_t part = need / 3 / sizeof(float);
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < 3; ++i) {
     p.pass[i].seg = workspace ? static_cast<float*>(workspace) + i * part : nullptr;
+    p.pass[i].rest = zero_rest >> i & 1;
+  }
   // dq_t = scale S_t do_t: the forward's direction over (dO, V, K), state transposed
   LinPass& a = p.pass[0];
   a.q = 3, a.k = 2, a.v = 1;
