@@ -389,7 +389,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  *
  * Tensors are bf16 [B, N, H, d] with strides, pointers and alignment as above (d = 64 or
  * 128); q has Hq heads and k Hk, any numbers; either may be 0 and its pointers NULL.  A
- * packed [T, H, d] batch is B = 1, N = T.  lengths: device int32 [B] or NULL (all N rows are
+ * packed [T, H, d] batch is B = 1, N = T (and lengths, where the buffer has more rows than its
+ * sequences, cu_seqlens + their number).  lengths: device int32 [B] or NULL (all N rows are
  * valid); rows at or past a sequence's length are not read and come out as exactly 0.  An
  * output may be the very tensor it is computed from (same pointer and strides); otherwise
  * inputs and outputs must not overlap, nor an output's elements one another.

@@ -585,11 +585,7 @@ def _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, leng
     if got is None:
         got = _remember(_qk_shapes, key, _qk_shape(ql and ql.shape, kl and kl.shape))
     head, rows, packed = got
-    lp = None
-    if lengths is not None:
-        if packed:
-            raise ValueError("a packed batch has no lengths: all of its rows are valid")
-        lp = _small(lengths, "lengths", torch.int32, head[:1], dev)
+    lp = _small(lengths, "lengths", torch.int32, head[:1], dev)
     d = head[4:]
     wqp, wkp = _small(wq, "wq", _f32, d, dev), _small(wk, "wk", _f32, d, dev)
     rot = n_sec = sa = sb = 0
@@ -636,7 +632,8 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, 
     weighted, and its first 2 * len(inv_freq) values rotated by the positions.  q, k bf16
     [B, N, H, d] or packed [T, H, d] (either may be None); wq, wk fp32 [d]; inv_freq fp64
     [pairs]; positions int32 [axes, B, N] resp. [axes, T] (one axis: that dimension may be
-    left out); sections: pairs of each axis.  Pad rows (lengths int32 [B]) come out as 0."""
+    left out); sections: pairs of each axis.  Pad rows (lengths int32 [B]) come out as 0; of a
+    packed batch all rows are valid, or the first lengths[0] (int32 [1], cu_seqlens[-1:])."""
     dev = _here()
     head, rot, ql, kl = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev)
     yq, yql = (None, None) if q is None else _out(out_q, q, ql, "out_q", dev)
@@ -659,7 +656,8 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
                      sections=None, interleaved: bool = False, lengths=None, norm: bool = True, dq=None, dk=None,
                      workspace=None, stream=None):
     """(dq, dk, dwq, dwk) from the gradients dyq, dyk of qk_norm_rope's outputs; dwq, dwk are
-    fp32 [d], None for a weight that is None.  ``workspace``: a contiguous CUDA buffer of
+    fp32 [d], None for a weight that is None.  Rows of a packed batch that hold no data (NaN,
+    say) must be behind lengths[0], or the weights' sums take them up.  ``workspace``: a contiguous CUDA buffer of
     qk_norm_rope_bwd_workspace_bytes bytes (allocated here if None and needed)."""
     dev = _here()
     head, rot, ql, kl = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev)
