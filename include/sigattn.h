@@ -393,7 +393,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  * sequences, cu_seqlens + their number).  lengths: device int32 [B] or NULL (all N rows are
  * valid); rows at or past a sequence's length are not read and come out as exactly 0.  An
  * output may be the very tensor it is computed from (same pointer and strides); otherwise
- * inputs and outputs must not overlap, nor an output's elements one another.
+ * inputs and outputs must not overlap, nor an output's elements one another (the pointer of
+ * the other side's tensor, or one's own with other strides, is refused).
  *
  * Backward: from dyq, dyk writes dq, dk (bf16; pad rows 0) and, where the pointers are not
  * NULL, dwq and dwk (fp32 [d], sums over all valid rows and heads, in an order that does not
@@ -402,8 +403,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  * 16-byte aligned, contents free on entry and undefined after; calls sharing one must not
  * overlap on the GPU.
  * Errors: INVALID (null pointer, B or N < 1, no heads, norm / interleaved not 0 or 1,
- * negative eps or stride, sections that do not add up, workspace missing or too small),
- * UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past 2^31 - 2^14, heads times head stride
+ * negative eps or stride, sections that do not add up, workspace missing or too small, an
+ * output in another tensor's place), UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past 2^31 - 2^14, heads times head stride
  * past 2^34 elements), ALIGNMENT, CUDA.
  */
 SIGATTN_API int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const int32_t* lengths,

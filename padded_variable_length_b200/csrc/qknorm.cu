@@ -555,6 +555,24 @@ int check_one(int H, const void* x, const int64_t* xs, const void* dy, const int
   return SIGATTN_OK;
 }
 
+// Whether an output is another tensor than the ones it is computed from, which it may be: the
+// queries' blocks and the keys' run side by side, so neither side's output may be the other's
+// input or output, nor a tensor of its own side with other strides.
+bool in_anothers_place(const QkParams& p) {
+  for (int i = 0; i < 2; ++i) {
+    const QkTensor &t = p.t[i], &other = p.t[1 - i];
+    if (t.H == 0) continue;
+    const auto moved = [&](int64_t sb, int64_t sn, int64_t sh) {  // (of steps that are taken)
+      return (p.tokens > p.N && sb != t.y_sb) || (p.N > 1 && sn != t.y_sn) ||
+             (t.H > 1 && sh != t.y_sh);
+    };
+    if (t.y == t.x && moved(t.x_sb, t.x_sn, t.x_sh)) return true;
+    if (t.y == t.dy && moved(t.dy_sb, t.dy_sn, t.dy_sh)) return true;
+    if (other.H > 0 && (t.y == other.x || t.y == other.dy || t.y == other.y)) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace sigattn
 
@@ -579,6 +597,7 @@ extern "C" int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const i
   if ((rc = check_one(Hk, k, k_strides, nullptr, nullptr, false, yk, yk_strides, wk, &p.t[1])) !=
       SIGATTN_OK)
     return rc;
+  if (in_anothers_place(p)) return SIGATTN_ERR_INVALID;
   return launch_qk<false>(p, static_cast<cudaStream_t>(s));
 }
 
@@ -620,6 +639,7 @@ extern "C" int sigattn_qk_norm_rope_bwd(
     if (reinterpret_cast<uintptr_t>(workspace) & 15u) return SIGATTN_ERR_ALIGNMENT;
     p.partial = static_cast<float*>(workspace);
   }
+  if (in_anothers_place(p)) return SIGATTN_ERR_INVALID;
   const cudaStream_t stream = static_cast<cudaStream_t>(s);
   rc = launch_qk<true>(p, stream);
   if (rc != SIGATTN_OK || !p.partial) return rc;
