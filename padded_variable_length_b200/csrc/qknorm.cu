@@ -25,8 +25,10 @@
 // zero rows); 64 single tokens 4.3 us, a launch.
 //
 // Angles: with inv_freq / 2 pi kept as a 64-bit fraction F of a turn, position * F modulo
-// 2^64 is the angle modulo one turn with no rounding that grows with the position, so far
-// positions are as exact as near ones (a 32-bit product is off by 1e-2 radians at 2e5).
+// 2^64 is the angle modulo one turn.  F is taken from a product in twice double's bits, so it is
+// off by 2^-63 of a turn at most and the angle of any int32 position by 2^-32, which is where
+// the sines take it: far positions are as exact as near ones (a 32-bit product is off by 1e-2
+// radians at 2e5; a double's, rounded, by 5e-7 inv_freq at the ends of int32).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -151,10 +153,15 @@ struct Lane {
         frac[x] = 0;
         axis[x] = 0;
         if (i < 4 ? turn0 : turn1) {
-          // inv_freq / 2 pi without its whole turns; scaling by 2^64 is exact
-          double f = p.inv_freq[pair] * 0.15915494309189533577;
+          // inv_freq / 2 pi as a sum of two doubles f + e (1 / 2 pi is one too), each without
+          // its whole turns; scaling by 2^64 is exact
+          const double v = p.inv_freq[pair], one = 0.15915494309189535, rest = -9.839338337591243e-18;
+          double f = v * one, e = fma(v, rest, fma(v, one, -f));
           f -= floor(f);
-          frac[x] = f < 1.0 ? static_cast<uint64_t>(f * 18446744073709551616.0) : 0;
+          e -= rint(e);
+          if (f < 1.0)  // (not of an infinity or a NaN)
+            frac[x] = static_cast<uint64_t>(f * 18446744073709551616.0) +
+                      static_cast<uint64_t>(__double2ll_rn(e * 18446744073709551616.0));
           while (axis[x] + 1 < p.axes && pair >= p.axis_end[axis[x]]) ++axis[x];
         }
       }
