@@ -150,6 +150,14 @@ __device__ __forceinline__ int valid_of(const Item& it, int c) {
   return min(kChunk, it.s.n - c * kChunk);
 }
 
+// Waits for the last of n phases of a ring of `len` barriers that falls to its x-th (none if there
+// is no such barrier, or no phase of it).
+__device__ __forceinline__ void wait_last(uint64_t* bars, int x, int n, int len,
+                                          const WaitCtx& w) {
+  if (x < len && x < n) mbar_wait(bars + x, (n - 1 - x) / len & 1, w);
+  __syncwarp();
+}
+
 template <int D, bool OUT, bool TWO>
 struct LinLayout {
   static constexpr int kBoxes = D / 64;
@@ -334,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* drain_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
   Item* items = reinterpret_cast<Item*>(smem + L::kItems);
   uint8_t* order = smem + L::kOrder;
-  const WaitCtx wctx{p.status, p.wait_ns, abort_flag};
+  const WaitCtx wctx{p.status, p.wait_ns, abort_flag}, drain{p.status, kDrainWaitNs, drain_flag};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -357,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(item_full + i, 1);
-      mbar_init(item_empty + i, OUT ? 22 : 17);  // the warps that take items
+      mbar_init(item_empty + i, OUT ? (p.cu ? 21 : 22) : 17);  // the warps that take items
     }
     *abort_flag = 0;
     *drain_flag = 0;
@@ -425,13 +433,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
     }
-    if (lane == 0) {
-      // Let the copies still in flight land before the CTA's shared memory goes away: always, as
-      // the warps that wait for them may give up after this one has issued its last.
-      const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
-      for (int u = max(0, t - ST); u < t; ++u) mbar_wait(qk_full + u % ST, (u / ST) & 1, drain);
-      for (int u = max(0, tv - VS); u < tv; ++u) mbar_wait(v_full + u % VS, (u / VS) & 1, drain);
-    }
+    // Let the copies still in flight land before the CTA's shared memory goes away: always, as the
+    // warps that wait for them may give up after this one has issued its last.  A lane for each
+    // barrier, which waits for its last phase.
+    t = __shfl_sync(0xFFFFFFFFu, t, 0);
+    tv = __shfl_sync(0xFFFFFFFFu, tv, 0);
+    const bool v = lane >= ST;
+    wait_last(v ? v_full : qk_full, v ? lane - ST : lane, v ? tv : t, v ? VS : ST, drain);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     // Four streams of products, each in chunk order; whichever has its operands goes next.
@@ -532,19 +540,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every MMA complete before the TMEM is released (also after an abort)
     mma_commit_w(done);
-    const WaitCtx drain{p.status, kDrainWaitNs, drain_flag};
     mbar_wait_w(done, 0, drain);
     // ... and every commit's arrival seen, as none may come when the CTA's shared memory is
     // another's: nobody else waits for the last ones of qk_empty and pv_done, and after an abort
-    // the warps that would have waited for s_full and u_full are gone
-    const int nqk = OUT ? to : tu, npv = OUT ? tp : tu;
-    for (int u = max(0, nqk - ST); u < nqk; ++u)
-      mbar_wait_w(qk_empty + u % ST, (u / ST) & 1, drain);
-    for (int u = max(0, npv - VS); u < npv; ++u)
-      mbar_wait_w(pv_done + u % VS, (u / VS) & 1, drain);
-    for (int u = max(0, ts - 2); u < ts; ++u) mbar_wait_w(s_full + (u & 1), (u >> 1) & 1, drain);
-    for (int u = max(0, tu - NU); u < tu; ++u)
-      mbar_wait_w(u_full + u % NU, (u / NU) & 1, drain);
+    // the warps that would have waited for s_full and u_full are gone.  A lane for each barrier.
+    int x = lane, n = OUT ? to : tu, len = ST;
+    uint64_t* bar = qk_empty;
+    if (x >= ST) x -= ST, n = OUT ? tp : tu, len = VS, bar = pv_done;
+    if (bar == pv_done && x >= VS) x -= VS, n = ts, len = 2, bar = s_full;
+    if (bar == s_full && x >= 2) x -= 2, n = tu, len = NU, bar = u_full;
+    wait_last(bar, x, n, len, drain);
   } else if (warp < kWarpV) {
     // ---------------------------------------------------------------- P = decayed, masked S
     if (OUT) {
@@ -834,33 +839,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpI + 1) {
     // ---------------------------------------------------------------- zero rows
     // Rows behind a padded sequence's last chunk, within the item's segment, are written as 0
-    // (those inside it come out of the chunk as 0); where asked, so are packed rows of no
-    // sequence, those from a sequence's end to the next one's start by its segments in equal
-    // parts, those before the first by the first's.
-    if (OUT) {
+    // (those inside it come out of the chunk as 0).
+    if (OUT && !p.cu) {
       Item it;
       for (int k = 0; take(k, it); ++k) {
         const LinPass& ps = p.pass[it.pass];
-        __nv_bfloat16* out = ps.out + it.s.tma_b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols +
-                             lane % 8 * 8;
-        int lo, hi;
-        if (!p.cu) {
-          lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk);
-          hi = it.seg == p.nseg - 1 ? p.N : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
-        } else if (ps.rest) {
-          lo = it.s.row0 + it.s.n;
-          hi = it.b + 1 < p.B ? max(lo, min(__ldg(p.cu + it.b + 1), p.T)) : p.T;
-          const int part = (hi - lo + p.nseg - 1) / p.nseg;
-          lo += it.seg * part;
-          hi = min(hi, lo + part);
-          if (it.b == 0 && it.seg == 0)
-            for (int r = lane / 8; r < it.s.row0; r += 4)
-              *reinterpret_cast<uint4*>(out + r * ps.o_sn) = make_uint4(0u, 0u, 0u, 0u);
-        } else {
-          continue;
-        }
+        const int lo = max(it.c0 * kChunk, (it.s.n + kChunk - 1) / kChunk * kChunk);
+        const int hi = it.seg == p.nseg - 1 ? p.N : min(p.N, (it.c0 + p.seg_chunks) * kChunk);
+        __nv_bfloat16* out =
+            ps.out + it.b * ps.o_sb + it.h * ps.o_sh + it.slice * kCols + lane % 8 * 8;
         for (int r = lo + lane / 8; r < hi; r += 4)
           *reinterpret_cast<uint4*>(out + r * ps.o_sn) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else if (OUT) {
+      // Packed rows of no sequence, where asked: before the first, from each one's end to the next
+      // one's start, behind the last.  Every CTA looks through all of them, a lane for each, and
+      // takes its share of rows, four at a time.  Following the items instead cost the other
+      // warps issue slots by its waits (gradients of documents without such rows 393 us, so 380);
+      // padded rows done this way come all at once (gradients of the padded batch 209 us, by
+      // the items 87).
+      int any = 0;
+      for (int i = 0; i < p.npass; ++i) any |= p.pass[i].rest;
+      for (int b0 = -1; any && b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        int lo = 0, hi = 0;
+        if (b < 0) {
+          hi = sequence(p, 0).row0;
+        } else if (b < p.B) {
+          const Seq s = sequence(p, b);
+          lo = s.row0 + s.n;
+          hi = b + 1 < p.B ? sequence(p, b + 1).row0 : p.T;
+        }
+        for (uint32_t left = __ballot_sync(0xFFFFFFFFu, lo < hi); left != 0u; left &= left - 1) {
+          const int from = __ffs(left) - 1;
+          const int end = __shfl_sync(0xFFFFFFFFu, hi, from);
+          int r = __shfl_sync(0xFFFFFFFFu, lo, from) + lane / 8;
+          for (r += blockIdx.x * 4; r < end; r += gridDim.x * 4)
+            for (int i = 0; i < p.npass; ++i) {
+              const LinPass& ps = p.pass[i];
+              __nv_bfloat16* out = ps.out + r * ps.o_sn + lane % 8 * 8;
+              for (int h = 0; ps.rest && h < p.H; ++h)
+                for (int x = 0; x < D; x += 64)
+                  *reinterpret_cast<uint4*>(out + h * ps.o_sh + x) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
       }
     }
   } else {
