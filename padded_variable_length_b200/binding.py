@@ -536,32 +536,25 @@ def _workspace(workspace, need: int, like: torch.Tensor, dev: int):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _in_order(call):
-    """A call that is given a stream runs with that stream as torch's current one: what it
-    allocates, zeroes or copies is then in the stream's order, as its kernels are, and not beside
-    work of the current stream that still uses the same memory.  The caller's tensors are kept
-    until the stream has run the call, and new ones until the current stream has used them."""
-    at = call.__code__.co_varnames[:call.__code__.co_argcount].index("stream")
-
-    @functools.wraps(call)
-    def run(*args, **kw):
-        stream = args[at] if len(args) > at else kw.get("stream")
-        if stream is None:
-            return call(*args, **kw)
-        if not isinstance(stream, torch.cuda.Stream):
-            handle = _stream(stream)  # 0 and 1 are names of the default stream
-            stream = torch.cuda.ExternalStream(handle) if handle not in (None, 0, 1) else torch.cuda.default_stream()
-        here = torch.cuda.current_stream()
-        with torch.cuda.stream(stream):
-            got = call(*args, **kw)
-        for t in (*args, *kw.values()):
-            if isinstance(t, _Tensor) and t.is_cuda:
-                t.record_stream(stream)
-        for t in got if isinstance(got, tuple) else (got,):
-            if t is not None:
-                t.record_stream(here)
-        return got
-    return run
+def _in_order(stream, call, args: dict):
+    """``call`` with these arguments and with the stream that it was given as torch's current
+    one: what it allocates, zeroes or copies is then in the stream's order, as its kernels are,
+    and not beside work of the current stream that still uses the same memory.  The caller's
+    tensors are kept until the stream has run the call, and new ones until the current stream
+    has used them."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # 0 and 1 are names of the default stream
+        stream = torch.cuda.ExternalStream(handle) if handle not in (None, 0, 1) else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        got = call(**{**args, "stream": None})
+    for t in args.values():
+        if isinstance(t, _Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(here)
+    return got
 
 
 def _qk_shape(qs, ks):
@@ -625,7 +618,6 @@ def _pair(t, lay):
     return (None, _NO_STRIDES) if t is None else (t.data_ptr(), lay.strides)
 
 
-@_in_order
 def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None, sections=None,
                  interleaved: bool = False, lengths=None, norm: bool = True, out_q=None, out_k=None, stream=None):
     """(yq, yk): every head of q and k normed by its root mean square (norm=False: not),
@@ -634,13 +626,15 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, 
     [pairs]; positions int32 [axes, B, N] resp. [axes, T] (one axis: that dimension may be
     left out); sections: pairs of each axis.  Pad rows (lengths int32 [B]) come out as 0; of a
     packed batch all rows are valid, or the first lengths[0] (int32 [1], cu_seqlens[-1:])."""
+    if stream is not None:
+        return _in_order(stream, qk_norm_rope, locals())
     dev = _here()
     head, rot, ql, kl = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev)
     yq, yql = (None, None) if q is None else _out(out_q, q, ql, "out_q", dev)
     yk, ykl = (None, None) if k is None else _out(out_k, k, kl, "out_k", dev)
     if head[0] and head[1] and head[2] + head[3]:
         _check(_lib.sigattn_qk_norm_rope(*head, *_pair(q, ql), *_pair(k, kl), *rot, *_pair(yq, yql), *_pair(yk, ykl),
-                                         _stream(stream)), "qk_norm_rope")
+                                         _stream(None)), "qk_norm_rope")
     return yq, yk
 
 
@@ -651,14 +645,16 @@ def qk_norm_rope_bwd_workspace_bytes(B: int, N: int, d: int) -> int:
     return n.value
 
 
-@_in_order
 def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_freq=None, positions=None,
                      sections=None, interleaved: bool = False, lengths=None, norm: bool = True, dq=None, dk=None,
                      workspace=None, stream=None):
     """(dq, dk, dwq, dwk) from the gradients dyq, dyk of qk_norm_rope's outputs; dwq, dwk are
     fp32 [d], None for a weight that is None.  Rows of a packed batch that hold no data (NaN,
-    say) must be behind lengths[0], or the weights' sums take them up.  ``workspace``: a contiguous CUDA buffer of
-    qk_norm_rope_bwd_workspace_bytes bytes (allocated here if None and needed)."""
+    say) must be behind lengths[0], or the weights' sums take them up.  ``workspace``: a
+    contiguous CUDA buffer of qk_norm_rope_bwd_workspace_bytes bytes (allocated here if None and
+    needed)."""
+    if stream is not None:
+        return _in_order(stream, qk_norm_rope_bwd, locals())
     dev = _here()
     head, rot, ql, kl = _qk_args(q, k, wq, wk, eps, inv_freq, positions, sections, interleaved, lengths, norm, dev)
     args, outs, grads = [], [], []
@@ -684,7 +680,7 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, inv_fr
     ws, wp, wn = _workspace(workspace, need, q if q is not None else k, dev)
     _check(_lib.sigattn_qk_norm_rope_bwd(*head, *_pair(q, ql), *_pair(k, kl), *args[0][:2], *args[1][:2], *rot,
                                          *args[0][2:], *args[1][2:], None if gq is None else gq.data_ptr(),
-                                         None if gk is None else gk.data_ptr(), wp, wn, _stream(stream)),
+                                         None if gk is None else gk.data_ptr(), wp, wn, _stream(None)),
            "qk_norm_rope_bwd")
     return outs[0], outs[1], gq, gk
 
@@ -734,7 +730,6 @@ def _hand_on(to: Optional[torch.Tensor], state: Optional[torch.Tensor]):
     return to
 
 
-@_in_order
 def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None,
                return_state: bool = False, scale: Optional[float] = None, out=None, final_state=None,
                workspace=None, stream=None):
@@ -744,6 +739,8 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
     sequences start from (None: 0).  The final state is returned where return_state is set or
     a buffer for it is given, else None.  Rows of no sequence come out as 0; of a packed tensor
     given as ``out`` they stay as they are."""
+    if stream is not None:
+        return _in_order(stream, linear_fwd, locals())
     dev = _here()
     head, (sp, fp), pairs, lay = _linear_args(q, ((k, "k"), (v, "v")), log_decay, lengths, cu_seqlens, max_seqlen,
                                               ((state, "state"), (final_state, "final_state")), dev)
@@ -759,16 +756,17 @@ def linear_fwd(q, k, v, log_decay, lengths=None, cu_seqlens=None, max_seqlen=Non
         return out.zero_() if rest else out, _hand_on(final_state, state)
     ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d), q, dev)
     _check(_lib.sigattn_linear_fwd_ex(*head, scale, *pairs, sp, out.data_ptr(), ol.strides, fp, rest, wp, wn,
-                                      _stream(stream)), "linear_fwd")
+                                      _stream(None)), "linear_fwd")
     return out, final_state
 
 
-@_in_order
 def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen=None, state=None, dstate=None,
                scale: Optional[float] = None, dq=None, dk=None, dv=None, dstate_out=None, workspace=None, stream=None):
     """(dq, dk, dv, dstate_out): gradients of linear_fwd from do and, for a loss that uses the
     final state, its gradient ``dstate``.  dstate_out, the gradient of ``state``, is None where
     there was no state (unless a buffer for it is given).  Rows of no sequence as in linear_fwd."""
+    if stream is not None:
+        return _in_order(stream, linear_bwd, locals())
     dev = _here()
     head, (sp, ep, gp), pairs, lay = _linear_args(
         q, ((k, "k"), (v, "v"), (do, "do")), log_decay, lengths, cu_seqlens, max_seqlen,
@@ -785,16 +783,17 @@ def linear_bwd(q, k, v, do, log_decay, lengths=None, cu_seqlens=None, max_seqlen
         return *(t.zero_() if rest >> i & 1 else t for i, t in enumerate((dq, dk, dv))), _hand_on(dstate_out, dstate)
     ws, wp, wn = _workspace(workspace, linear_workspace_bytes(B, N, H, d, True), q, dev)
     _check(_lib.sigattn_linear_bwd_ex(*head, scale, *pairs, sp, ep, dq.data_ptr(), dql.strides, dk.data_ptr(), dkl.strides,
-                                      dv.data_ptr(), dvl.strides, gp, rest, wp, wn, _stream(stream)), "linear_bwd")
+                                      dv.data_ptr(), dvl.strides, gp, rest, wp, wn, _stream(None)), "linear_bwd")
     return dq, dk, dv, dstate_out
 
 
-@_in_order
 def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] = None, state_out=None, out=None,
                 stream=None) -> torch.Tensor:
     """o of one token of each sequence, q, k, v bf16 [B, H, d]; ``state`` fp32 [B, H, d, d] is
     updated in place, or kept and its update written to ``state_out``.  Sequences with
     lengths[b] = 0 have no token: o is 0 and their state stays."""
+    if stream is not None:
+        return _in_order(stream, linear_step, locals())
     dev = _here()
     ql, kl, vl = _tensor(q, "q", dev, (3,)), _tensor(k, "k", dev, (3,)), _tensor(v, "v", dev, (3,))
     if kl.shape != ql.shape or vl.shape != ql.shape:
@@ -813,7 +812,7 @@ def linear_step(q, k, v, log_decay, state, lengths=None, scale: Optional[float] 
     if q.numel() == 0:
         return out
     _check(_lib.sigattn_linear_step(B, H, d, lp, gp, scale, q.data_ptr(), ql.strides2, k.data_ptr(), kl.strides2,
-                                    v.data_ptr(), vl.strides2, sp, np_, out.data_ptr(), ol.strides2, _stream(stream)),
+                                    v.data_ptr(), vl.strides2, sp, np_, out.data_ptr(), ol.strides2, _stream(None)),
            "linear_step")
     return out
 
