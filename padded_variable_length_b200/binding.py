@@ -289,14 +289,37 @@ def tile_list_check_host(t: dict, run_ptr=None, runs=None) -> int:
     return where.value
 
 
+def _in_order(stream, call, args: dict):
+    """``call`` with these arguments and with the stream that it was given as torch's current
+    one: what it allocates, zeroes or copies is then in the stream's order, as its kernels are,
+    and not beside work of the current stream that still uses the same memory.  The caller's
+    tensors are kept until the stream has run the call, and new ones until the current stream
+    has used them."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # 0 and 1 are names of the default stream
+        stream = torch.cuda.ExternalStream(handle) if handle not in (None, 0, 1) else torch.cuda.default_stream()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        got = call(**{**args, "stream": None})
+    for t in args.values():
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(here)
+    return got
+
+
 def bias_from_counts(counts: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """b = -log(n) per query row from the int32 counts n (0 where n = 0)."""
+    if stream is not None:
+        return _in_order(stream, bias_from_counts, locals())
     if counts.dtype != torch.int32 or not counts.is_cuda or not counts.is_contiguous():
         raise ValueError("counts must be a contiguous int32 CUDA tensor")
     if out is None:
         out = torch.empty(counts.shape, dtype=torch.float32, device=counts.device)
     _check(_lib.sigattn_bias_from_counts(counts.data_ptr(), counts.numel(), out.data_ptr(),
-                                         _stream(stream)), "bias_from_counts")
+                                         _stream(None)), "bias_from_counts")
     return out
 
 
@@ -356,6 +379,8 @@ def _check_extents(plan: "Plan", q_side, k_side, bias=None, lse=None, workspace=
 def fwd(plan: Plan, q, k, v, bias=None, epilogue: int = SIGMOID, scale: Optional[float] = None,
         out=None, lse=None, stream=None):
     """O (and the row log-normaliser for the softmax modes) of the planned attention."""
+    if stream is not None:
+        return _in_order(stream, fwd, locals())
     B, Nq, H, d = _shape(plan, q)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
@@ -368,7 +393,7 @@ def fwd(plan: Plan, q, k, v, bias=None, epilogue: int = SIGMOID, scale: Optional
     _check(_lib.sigattn_fwd(plan.handle, epilogue, H, d, float(scale),
                             q.data_ptr(), _strides(q), k.data_ptr(), _strides(k),
                             v.data_ptr(), _strides(v), bp, bs, out.data_ptr(), _strides(out),
-                            lse.data_ptr() if lse is not None else None, _stream(stream)), "fwd")
+                            lse.data_ptr() if lse is not None else None, _stream(None)), "fwd")
     return out, lse
 
 
@@ -379,6 +404,8 @@ def bwd(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, lse=None
         scale: Optional[float] = None, workspace=None, dq=None, dk=None, dv=None, stream=None,
         parts: int = BWD_ALL):
     """dQ, dK, dV of L = sum(dO * O) (``parts`` selects PREP / DKDV / DQ)."""
+    if stream is not None:
+        return _in_order(stream, bwd, locals())
     B, Nq, H, d = _shape(plan, q)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
@@ -398,7 +425,7 @@ def bwd(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, lse=None
                                bp, bs, lse.data_ptr() if lse is not None else None,
                                workspace.data_ptr() if workspace is not None else None,
                                dq.data_ptr(), _strides(dq), dk.data_ptr(), _strides(dk),
-                               dv.data_ptr(), _strides(dv), int(parts), _stream(stream)), "bwd")
+                               dv.data_ptr(), _strides(dv), int(parts), _stream(None)), "bwd")
     return dq, dk, dv
 
 
@@ -414,6 +441,8 @@ def bwd_fused(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, ls
     """dQ, dK, dV of L = sum(dO * O) in one walk over the k-tile columns (d = 64): dQ is
     accumulated in fp32 in ``workspace`` (a 16-byte aligned CUDA buffer of at least
     bwd_fused_workspace_bytes bytes; allocated here if None) and converted at the end."""
+    if stream is not None:
+        return _in_order(stream, bwd_fused, locals())
     B, Nq, H, d = _shape(plan, q)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
@@ -434,7 +463,7 @@ def bwd_fused(plan: Plan, q, k, v, o, do, bias=None, epilogue: int = SIGMOID, ls
                                   bp, bs, lse.data_ptr() if lse is not None else None,
                                   workspace.data_ptr(), nbytes,
                                   dq.data_ptr(), _strides(dq), dk.data_ptr(), _strides(dk),
-                                  dv.data_ptr(), _strides(dv), _stream(stream)), "bwd_fused")
+                                  dv.data_ptr(), _strides(dv), _stream(None)), "bwd_fused")
     return dq, dk, dv
 
 
@@ -534,27 +563,6 @@ def _workspace(workspace, need: int, like: torch.Tensor, dev: int):
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the current CUDA device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _in_order(stream, call, args: dict):
-    """``call`` with these arguments and with the stream that it was given as torch's current
-    one: what it allocates, zeroes or copies is then in the stream's order, as its kernels are,
-    and not beside work of the current stream that still uses the same memory.  The caller's
-    tensors are kept until the stream has run the call, and new ones until the current stream
-    has used them."""
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)  # 0 and 1 are names of the default stream
-        stream = torch.cuda.ExternalStream(handle) if handle not in (None, 0, 1) else torch.cuda.default_stream()
-    here = torch.cuda.current_stream()
-    with torch.cuda.stream(stream):
-        got = call(**{**args, "stream": None})
-    for t in args.values():
-        if isinstance(t, _Tensor) and t.is_cuda:
-            t.record_stream(stream)
-    for t in got if isinstance(got, tuple) else (got,):
-        if t is not None:
-            t.record_stream(here)
-    return got
 
 
 def _qk_shape(qs, ks):
