@@ -377,6 +377,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  * valid token and head, x the head's d values:
  *     u = x / sqrt(mean(x^2) + eps)   (norm = 1; norm = 0: u = x and eps is not used)
  *     y = R (w * u)                   w fp32 [d], shared by the tensor's heads; NULL: all 1
+ * (squares are summed in fp32: u is 0 for a head with values past 1e18, and with eps = 0 it is
+ * NaN, as 0 / 0 is, for a head of zeros).
  * R turns the pairs of the first rot_dim values (a multiple of 16 up to d; 0: no rotation)
  * and passes the others: pair p (a, b) becomes (a cos t - b sin t, a sin t + b cos t) with
  * t = position * inv_freq[p].  interleaved 0: pair p is (x[p], x[p + rot_dim/2]); 1: it is
@@ -384,8 +386,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  * HOST array of `axes` counts that add up to rot_dim/2) says how many consecutive pairs each
  * axis turns.  positions: device int32, of axis a, batch entry b and row i at
  * a * pos_stride_axis + b * pos_stride_b + i, any value, negative ones included; angles are
- * taken modulo a turn in 64 bits, so they are as exact far out as near.  inv_freq: device
- * fp64 [rot_dim/2], radians per position.
+ * taken modulo a turn in 64 bits, to 2^-32 of a turn, so they are as exact far out as near.
+ * inv_freq: device fp64 [rot_dim/2], radians per position.
  *
  * Tensors are bf16 [B, N, H, d] with strides, pointers and alignment as above (d = 64 or
  * 128); q has Hq heads and k Hk, any numbers; either may be 0 and its pointers NULL.  A
@@ -404,8 +406,8 @@ SIGATTN_API int sigattn_bwd_noalloc(const sigattn_plan* plan, int epilogue, int 
  * overlap on the GPU.
  * Errors: INVALID (null pointer, B or N < 1, no heads, norm / interleaved not 0 or 1,
  * negative eps or stride, sections that do not add up, workspace missing or too small, an
- * output in another tensor's place), UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past 2^31 - 2^14, heads times head stride
- * past 2^34 elements), ALIGNMENT, CUDA.
+ * output in another tensor's place), UNSUPPORTED (d, rot_dim, more than 4 axes, B * N past
+ * 2^31 - 2^14, heads times head stride past 2^34 elements), ALIGNMENT, CUDA.
  */
 SIGATTN_API int sigattn_qk_norm_rope(int B, int N, int Hq, int Hk, int d, const int32_t* lengths,
                                      const void* q, const int64_t q_strides[3],
