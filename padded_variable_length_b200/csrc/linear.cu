@@ -20,14 +20,16 @@
 //
 // What it has to move: q, k, v and o once (the backward seven tensors; its passes read ten, the
 // two that run side by side sharing their reads through L2).  What bounds it is waiting: with full
-// lengths (16 x 2048, 16 heads of 128) DRAM is 53 % busy, the tensor pipe 36 %, shared memory's
-// banks 24 % (reads) and 14 % (writes), the issue slots 50 %.  A chunk's jobs hang on each other
+// lengths (16 x 2048, 16 heads of 128) DRAM is 56 % busy, the tensor pipe 37 %, shared memory's
+// banks 24 % (reads) and 15 % (writes), the issue slots 51 %.  A chunk's jobs hang on each other
 // (the weights of a warp whose rows see all keys take 2300 of a chunk's 3600 cycles), and its
 // loads, 2200 to 5600 cycles, on the products that free their stage.  With Q R in two buffers, so
 // that it need not wait for the outputs of the chunk before, and the issuer's tests side by side,
 // the long ragged batch (8 x 4096..16384, 16 heads of 128) went from 303 to 292 us and the
 // gradients of the documents below from 335 to 316; 287 us is 3500 cycles a chunk on the SM with
-// the most, 153, and the copy of its tensors 233.
+// the most, 153, and the copy of its tensors 233.  (All times here are of 20 calls in a row at
+// 1965 MHz.  After a second of them the power cap holds the clock at 1400 to 1550 MHz: the long
+// batch then takes 337 us, the documents' gradients 377.)
 // Layout: 128 tokens a chunk are the M of every product; d = 128 is cut into two items of 64
 // value columns, because all of its operands fit shared memory twice that way (one item of 128
 // columns leaves K and Q single stages, whose copies nothing hides: 553 us).
@@ -301,8 +303,8 @@ __device__ __forceinline__ void weigh_near(const uint32_t (&s)[16], float l2, bo
 // accuracy a rounded V' would cost (2^-9 instead of 2^-18).  Where the state only serves the
 // outputs, for which it is rounded to bf16 anyway, V' is rounded once: the outputs are 2.6e-3
 // off instead of 2.3e-3 (relative, 2-norm; their own rounding is 1.7e-3), the long ragged batch
-// takes 303 us instead of 328, gradients of 64 documents (32768 tokens, 16 heads of 128) 357
-// instead of 430.
+// took 303 us instead of 328 when it was changed, gradients of 64 documents (32768 tokens, 16
+// heads of 128) 357 instead of 430.
 //
 // Warps: 0 copies, 1 issues the products, the last two decode the work items and zero the pad
 // rows (at their own pace: written by the outputs' warps after an item's last chunk they held

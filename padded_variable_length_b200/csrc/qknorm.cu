@@ -19,10 +19,12 @@
 // in flight and few enough instructions are issued: each lane keeps the pieces of its next
 // kDepth - 1 steps on their way into shared memory slots of its own (cp.async; nobody else
 // reads them, so a step waits for its own copies alone), and arithmetic is done on pairs.
-// Measured: 16 + 16 heads of 128 at 32768 tokens, backward, 137 us (5.9 TB/s, 89 % of the copy
-// rate; with plain loads one step ahead at most 303); 8 + 8 heads of 64 on a padded batch of
-// 32 x 2048 with 26000 valid rows, forward without rotation, 35 us (5.2 TB/s, 79 %: most of it
-// zero rows); 64 single tokens 4.3 us, a launch.
+// Measured (20 calls in a row, 1965 MHz): 16 + 16 heads of 128 at 32768 tokens, backward, 138 us
+// (5.8 TB/s, 89 % of the copy rate; 155 us once the power cap holds the clock at 1717 MHz; with
+// plain loads one step ahead at most 303); 8 + 8 heads of 64 on a padded batch of 32 x 2048 with
+// 23676 valid rows, forward without rotation, 35 us (5.2 TB/s, 79 %: 18.6 for these rows packed,
+// as long as torch.neg over them, and the rest for the zero rows); 64 single tokens 4.3 us, a
+// launch.
 //
 // Angles: with inv_freq / 2 pi kept as a 64-bit fraction F of a turn, position * F modulo
 // 2^64 is the angle modulo one turn.  F is taken from a product in twice double's bits, so it is
