@@ -474,8 +474,8 @@ SIGATTN_API int sigattn_qk_norm_rope_bwd(int B, int N, int Hq, int Hk, int d,
  *
  * Errors: INVALID (null pointer, B, N, H or T < 1, both lengths and cu_seqlens, non-finite
  * scale, zero_rest of other bits, workspace missing or too small, states that overlap where
- * they must not, an output that is an input), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT, NO_DEVICE, CUDA; TIMEOUT
- * through sigattn_get_status.
+ * they must not, an output that is an input), UNSUPPORTED (d, B * H past 2^28), ALIGNMENT,
+ * NO_DEVICE, CUDA; TIMEOUT through sigattn_get_status.
  */
 SIGATTN_API int sigattn_linear_workspace_size(int B, int N, int H, int d, int backward,
                                               size_t* bytes);
